@@ -122,6 +122,16 @@ SIGNATURES = [
      [_c.POINTER(GsParams), _c.POINTER(GsGrads), _c.POINTER(GsGrads), _vp, _vp, _vp,
       _c.POINTER(GsDensifyParams), _c.POINTER(GsGrads), _c.POINTER(GsGrads), _c.POINTER(GsGrads),
       _c.c_int64, _vp, _vp, _vp, _c.c_size_t, _vp]),
+    ("gs_blend_weights_workspace_size", _c.c_size_t, [_c.c_int64]),
+    ("gs_blend_weights", _c.c_int,
+     [_c.POINTER(GsProjected), _c.POINTER(GsBinned), _c.POINTER(GsCamera), _c.c_int32,
+      _c.c_int64, _vp, _vp, _vp, _c.c_float, _vp, _vp, _vp, _c.c_size_t, _vp]),
+    ("gs_evict_workspace_size", _c.c_size_t, [_c.c_int64]),
+    ("gs_evict_select", _c.c_int,
+     [_vp, _vp, _c.c_int64, _c.c_int64, _vp, _vp, _c.c_size_t, _vp]),
+    ("gs_evict_compact", _c.c_int,
+     [_c.POINTER(GsParams), _c.POINTER(GsGrads), _c.POINTER(GsGrads), _vp, _c.POINTER(GsGrads),
+      _c.POINTER(GsGrads), _c.POINTER(GsGrads), _c.c_int64, _vp, _vp, _vp, _c.c_size_t, _vp]),
     ("gs_l1_dssim_workspace_size", _c.c_size_t, [_c.c_int32]),
     ("gs_l1_dssim", _c.c_int,
      [_vp, _vp, _c.c_int32, _c.c_int32, _c.c_int32, _c.c_float, _vp, _vp, _vp, _c.c_size_t,
@@ -350,6 +360,49 @@ def gs_densify_and_prune(params: GsParams, m_in: GsGrads, v_in: GsGrads, accum, 
                                       int(out_capacity), _ptr(n_out), _ptr(codes), _ptr(ws),
                                       int(ws.numel() * ws.element_size()), _stream(stream)),
            "gs_densify_and_prune")
+
+
+def gs_blend_weights_workspace_size(n: int) -> int:
+    return int(lib().gs_blend_weights_workspace_size(int(n)))
+
+
+def gs_blend_weights(proj: GsProjected, bins: GsBinned, cams_arr, n_views: int, n: int,
+                     n_contrib, weight_sum, ws, weight_max=None, warp_masks=None,
+                     pixel_weight=None, decay: float = 1.0, stream=None) -> None:
+    """Per-Gaussian sums (and maxima) of the frame's blending weights, added
+    to decay times what weight_sum (weight_max) holds; pixel_weight: optional
+    float32 [V, H, W] in [0, 1]; n_contrib and warp_masks: the forward's."""
+    _check(lib().gs_blend_weights(_c.byref(proj), _c.byref(bins), cams_arr, int(n_views), int(n),
+                                  _ptr(n_contrib), _ptr(warp_masks), _ptr(pixel_weight),
+                                  float(decay), _ptr(weight_sum), _ptr(weight_max), _ptr(ws),
+                                  int(ws.numel() * ws.element_size()), _stream(stream)),
+           "gs_blend_weights")
+
+
+def gs_evict_workspace_size(n: int) -> int:
+    return int(lib().gs_evict_workspace_size(int(n)))
+
+
+def gs_evict_select(score, protect, n: int, n_keep: int, decisions, ws, stream=None) -> None:
+    """decisions int8 [n]: 1 for the n_keep best by (protected, score, lowest
+    index), 0 for the others; protect: uint8 [n] or None."""
+    _check(lib().gs_evict_select(_ptr(score), _ptr(protect), int(n), int(n_keep),
+                                 _ptr(decisions), _ptr(ws), int(ws.numel() * ws.element_size()),
+                                 _stream(stream)), "gs_evict_select")
+
+
+def gs_evict_compact(params: GsParams, m_in: Optional[GsGrads], v_in: Optional[GsGrads],
+                     decisions, out: GsGrads, m_out: Optional[GsGrads],
+                     v_out: Optional[GsGrads], out_capacity: int, ws, source=None, n_out=None,
+                     stream=None) -> None:
+    """Survivors' rows in index order; source: optional int32 [out_capacity]
+    input indices; n_out: optional int64 [1]."""
+    ref = lambda g: None if g is None else _c.byref(g)  # noqa: E731
+    _check(lib().gs_evict_compact(_c.byref(params), ref(m_in), ref(v_in), _ptr(decisions),
+                                  _c.byref(out), ref(m_out), ref(v_out), int(out_capacity),
+                                  _ptr(source), _ptr(n_out), _ptr(ws),
+                                  int(ws.numel() * ws.element_size()), _stream(stream)),
+           "gs_evict_compact")
 
 
 def gs_l1_dssim_workspace_size(n_views: int) -> int:

@@ -634,6 +634,112 @@ gs_status gs_densify_and_prune(const gs_params* in, const gs_grads* m_in, const 
       reinterpret_cast<uint32_t*>(w + kStatusOffset), op, om, ov, st));
 }
 
+size_t gs_blend_weights_workspace_size(int64_t n) {
+  if (n < 0 || n >= (1ll << 31)) return 0;
+  return align_up(kControlBytes + (size_t)n * sizeof(uint64_t));  // fixed-point totals
+}
+
+gs_status gs_blend_weights(const gs_projected* proj, const gs_binned* bins, const gs_camera* cams,
+                           int32_t n_views, int64_t n, const uint32_t* n_contrib,
+                           const uint8_t* warp_masks, const float* pixel_weight, float decay,
+                           float* weight_sum, float* weight_max, void* ws, size_t ws_bytes,
+                           void* stream) {
+  if (!proj || !bins || !check_cams(cams, n_views) || !status_ws_ok(ws))
+    return GS_ERR_INVALID_ARG;
+  if (n < 0 || bins->pair_capacity < 0 || !(decay >= 0.f && decay <= 1.f))
+    return GS_ERR_INVALID_ARG;
+  if (n >= (1ll << 31)) return GS_ERR_OVERFLOW;
+  const Grid g = grid_of(cams[0]);
+  // a total counts every pixel at most once, in units of 2^-32 of 64 bits
+  if ((int64_t)g.width * g.height > (1ll << 31) / n_views) return GS_ERR_OVERFLOW;
+  if (ws_bytes < gs_blend_weights_workspace_size(n)) return GS_ERR_INVALID_ARG;
+  if (n == 0) return GS_OK;
+  if (!proj->records || !aligned(proj->records, 16) || !bins->ids || !bins->ranges ||
+      !n_contrib || !weight_sum)
+    return GS_ERR_INVALID_ARG;
+  if (!aligned(bins->ids, 4) || !aligned(bins->ranges, 8) || !aligned(n_contrib, 4) ||
+      !aligned(pixel_weight, 4) || !aligned(weight_sum, 4) || !aligned(weight_max, 4))
+    return GS_ERR_INVALID_ARG;
+  uint64_t* sums = reinterpret_cast<uint64_t*>(static_cast<unsigned char*>(ws) + kControlBytes);
+  return cuda_status(launch_blend_weights(
+      proj->records, bins->ids, bins->ranges, bins->pair_capacity, g, n_views, (int)n, n_contrib,
+      warp_masks, pixel_weight, decay, weight_sum, weight_max, sums, status_word(ws),
+      wait_cfg(GS_STALL_RASTER_FWD), static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+constexpr size_t kEvictNOutOffset = 256;  // int64, when the caller passes none
+
+gsb::EvictScratch evict_scratch(void* ws, int64_t n) {
+  unsigned char* w = static_cast<unsigned char*>(ws);
+  gsb::EvictScratch s{};
+  s.state = reinterpret_cast<gsb::EvictState*>(w + kControlBytes);
+  s.groups = reinterpret_cast<uint32_t*>(s.state + 1);
+  s.counts = s.groups + gsb::evict_groups(n);
+  return s;
+}
+}  // namespace
+
+size_t gs_evict_workspace_size(int64_t n) {
+  if (n < 0 || n >= (1ll << 31)) return 0;
+  return align_up(kControlBytes + sizeof(gsb::EvictState) +
+                  (size_t)(gsb::evict_groups(n) + gsb::evict_blocks(n)) * sizeof(uint32_t));
+}
+
+gs_status gs_evict_select(const float* score, const uint8_t* protect, int64_t n, int64_t n_keep,
+                          int8_t* decisions, void* ws, size_t ws_bytes, void* stream) {
+  if (n < 0 || n_keep < 0 || !status_ws_ok(ws)) return GS_ERR_INVALID_ARG;
+  if (n >= (1ll << 31)) return GS_ERR_OVERFLOW;
+  if (ws_bytes < gs_evict_workspace_size(n)) return GS_ERR_INVALID_ARG;
+  if (n == 0) return GS_OK;
+  if (!score || !decisions || !aligned(score, 4)) return GS_ERR_INVALID_ARG;
+  return cuda_status(gsb::launch_evict_select(score, protect, (int)n,
+                                              (int)(n_keep < n ? n_keep : n), decisions,
+                                              evict_scratch(ws, n),
+                                              static_cast<cudaStream_t>(stream)));
+}
+
+gs_status gs_evict_compact(const gs_params* in, const gs_grads* m_in, const gs_grads* v_in,
+                           const int8_t* decisions, gs_grads* out, gs_grads* m_out,
+                           gs_grads* v_out, int64_t out_capacity, uint32_t* source,
+                           int64_t* n_out, void* ws, size_t ws_bytes, void* stream) {
+  if (!in || !out || !status_ws_ok(ws)) return GS_ERR_INVALID_ARG;
+  if (in->n < 0 || in->sh_degree < 0 || in->sh_degree > 3 || out_capacity < 0)
+    return GS_ERR_INVALID_ARG;
+  if (in->n >= (1ll << 31) || out_capacity >= (1ll << 31)) return GS_ERR_OVERFLOW;
+  // both moments or neither, each with its output
+  const bool moments = m_in != nullptr;
+  if ((v_in != nullptr) != moments || (m_out != nullptr) != moments ||
+      (v_out != nullptr) != moments)
+    return GS_ERR_INVALID_ARG;
+  if (ws_bytes < gs_evict_workspace_size(in->n)) return GS_ERR_INVALID_ARG;
+  if (!aligned(n_out, 8) || !aligned(source, 4)) return GS_ERR_INVALID_ARG;
+  int64_t* count = n_out ? n_out
+                         : reinterpret_cast<int64_t*>(static_cast<unsigned char*>(ws) +
+                                                      kEvictNOutOffset);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int n = (int)in->n;
+  if (n == 0) return cuda_status(cudaMemsetAsync(count, 0, sizeof(int64_t), st));
+  if (!decisions) return GS_ERR_INVALID_ARG;
+  gs_grads pin{const_cast<float*>(in->means), const_cast<float*>(in->log_scales),
+               const_cast<float*>(in->quats), const_cast<float*>(in->opacity_logit),
+               const_cast<float*>(in->sh)};
+  // quantised SH: the SH state is gs_densify_sh_quant's, from the same decisions
+  const bool with_sh = in->sh_quant == nullptr;
+  gsb::DpTensorPtrs tp{}, tm{}, tv{}, op{}, om{}, ov{};
+  if (!params_sh_ok(*in) || !dp_tensors(&pin, true, with_sh, tp) ||
+      !dp_tensors(m_in, false, with_sh, tm) || !dp_tensors(v_in, false, with_sh, tv))
+    return GS_ERR_INVALID_ARG;
+  if (out_capacity > 0 &&
+      (!dp_tensors(out, true, with_sh, op) || !dp_tensors(m_out, false, with_sh, om) ||
+       !dp_tensors(v_out, false, with_sh, ov)))
+    return GS_ERR_INVALID_ARG;
+  const int k3 = with_sh ? 3 * (in->sh_degree + 1) * (in->sh_degree + 1) : 0;
+  return cuda_status(gsb::launch_evict_compact(tp, tm, tv, decisions, n, k3, op, om, ov,
+                                               out_capacity, source, count, evict_scratch(ws, n),
+                                               status_word(ws), st));
+}
+
 size_t gs_l1_dssim_workspace_size(int32_t n_views) {
   if (n_views < 0) return 0;
   return (size_t)n_views * 2 * sizeof(double) + 16;

@@ -133,6 +133,13 @@ cudaError_t launch_raster_bwd(const float* records, const uint32_t* ids, const i
                               const uint32_t* n_contrib, const uint8_t* warp_masks,
                               float* grad2d, uint32_t* status, const WaitCfg& wc,
                               cudaStream_t stream);
+// Accumulated blending weights: `sums` is n 64-bit words of scratch.
+cudaError_t launch_blend_weights(const float* records, const uint32_t* ids, const int64_t* ranges,
+                                 int64_t capacity, const Grid& g, int n_views, int n,
+                                 const uint32_t* n_contrib, const uint8_t* warp_masks,
+                                 const float* pixel_weight, float decay, float* weight_sum,
+                                 float* weight_max, uint64_t* sums, uint32_t* status,
+                                 const WaitCfg& wc, cudaStream_t stream);
 cudaError_t launch_densify(const float* grad2d, const int* radii, int n_views, int n,
                            float* accum_plain, float* accum_abs, int* denom, cudaStream_t stream);
 cudaError_t launch_adam(const gs_adam_group* groups, int n_groups, float b1, float b2, float eps,
@@ -171,6 +178,32 @@ cudaError_t launch_densify_and_prune(const DpTensorPtrs& p_in, const DpTensorPtr
                                      uint32_t* status, const DpTensorPtrs& p_out,
                                      const DpTensorPtrs& m_out, const DpTensorPtrs& v_out,
                                      cudaStream_t stream);
+
+// Eviction under a budget (evict.cu).
+struct EvictState {
+  uint32_t hist[3][2048];  // key digits of each pass, the most significant first
+  uint32_t done[3];        // blocks that finished a pass
+  uint32_t prefix;         // key digits found so far: the threshold key at the end
+  uint32_t rank;           // survivors still to come from the keys that share them
+  uint32_t equal;          // keys equal to the threshold
+  uint32_t reserved[2];
+};
+struct EvictScratch {
+  EvictState* state;
+  uint32_t* groups;  // [evict_groups(n)], right behind the state
+  uint32_t* counts;  // [evict_blocks(n)]
+};
+int64_t evict_blocks(int64_t n);
+int64_t evict_groups(int64_t n);
+cudaError_t launch_evict_select(const float* score, const uint8_t* protect, int n, int n_keep,
+                                int8_t* decisions, const EvictScratch& w, cudaStream_t stream);
+// m_in / v_in with NULL arrays: no moments. k3 0: no SH.
+cudaError_t launch_evict_compact(const DpTensorPtrs& p_in, const DpTensorPtrs& m_in,
+                                 const DpTensorPtrs& v_in, const int8_t* decisions, int n, int k3,
+                                 const DpTensorPtrs& p_out, const DpTensorPtrs& m_out,
+                                 const DpTensorPtrs& v_out, int64_t capacity, uint32_t* source,
+                                 int64_t* n_out, const EvictScratch& w, uint32_t* status,
+                                 cudaStream_t stream);
 
 // Fused L1 + D-SSIM loss over [n_views][3][H][W] planes; `sums` holds
 // 2 * n_views doubles followed by the block counter `done` (both cleared here).

@@ -751,6 +751,214 @@ __global__ void __launch_bounds__(Shape<NP>::kThreads) k_raster_bwd(
       mbar_wait_bounded(&s_bar[bf], (uint32_t)((pend[bf] >> 1) & 1), wc.limit_ns, status);
 }
 
+// Accumulated blending weights (gs_blend_weights): per list entry the sum (and
+// the largest) over the tile's pixels of m w, w = alpha T the forward's weight
+// and m the pixel's weight in [0, 1]. The walk is the forward's without the
+// colours and without its stop test: n_contrib already says how far each
+// pixel composited. A warp sums its 64 pixels by shuffles, the block its four
+// warps in a fixed order, and one 64-bit integer reduction per (tile, entry)
+// adds the sum in units of 2^-32 to the Gaussian's total, so totals do not
+// depend on the order in which tiles arrive; a maximum of non-negative floats
+// is a maximum of their bits.
+constexpr float kWeightUnit = 4294967296.f;  // 2^32
+
+template <int NP>
+__global__ void __launch_bounds__(Shape<NP>::kThreads) k_blend_weights(
+    const float* __restrict__ records, const uint32_t* __restrict__ ids,
+    const int64_t* __restrict__ ranges, RasterGeom geo, const uint32_t* __restrict__ n_contrib,
+    const uint8_t* __restrict__ wmask_in, const float* __restrict__ pixel_weight,
+    unsigned long long* __restrict__ sums, uint32_t* __restrict__ largest,
+    uint32_t* __restrict__ status, WaitCfg wc) {
+  using Sh = Shape<NP>;
+  constexpr int kBatch = Sh::kBatch;
+  constexpr int kWarps = Sh::kWarps;
+  __shared__ __align__(128) float s_rec[2][kBatch][GS_RECORD_FLOATS];
+  __shared__ float s_sum[kWarps][kBatch];
+  __shared__ float s_max[kWarps][kBatch];
+  __shared__ uint32_t s_id[2][kBatch];
+  __shared__ __align__(8) uint64_t s_bar[2];
+  __shared__ uint32_t s_wmax[kWarps];
+  __shared__ uint8_t s_mask[kBatch];
+  __shared__ uint8_t s_list[kWarps][kBatch];
+
+  const int tile = blockIdx.x;
+  const TilePix<NP> tp = tile_pixel<NP>(geo.g, tile);
+  const size_t hw = (size_t)geo.g.width * geo.g.height;
+  int64_t start, end;
+  tile_range(ranges, tile, geo.capacity, start, end, status);
+  const float* rec_view = records + (size_t)tp.view * geo.n * GS_RECORD_FLOATS;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool stalled = (int64_t)tile == wc.stall;  // test hook, see k_raster_fwd
+
+  // a pixel without weight takes no part (a NaN or negative weight counts as
+  // none, and as 0 in the products: -inf times 0 would be NaN)
+  float2 T[NP], pw[NP];
+  uint32_t nc[2 * NP], mine = 0;
+#pragma unroll
+  for (int q = 0; q < NP; ++q) {
+    T[q] = f2(1.f);
+    pw[q] = f2(1.f);
+  }
+#pragma unroll
+  for (int i = 0; i < 2 * NP; ++i) {
+    nc[i] = 0;
+    if (!tp.in[i]) continue;
+    const size_t pix = (size_t)tp.view * hw + (size_t)(tp.py + 4 * i) * geo.g.width + tp.px;
+    nc[i] = n_contrib[pix];
+    if (pixel_weight) {
+      const float m = pixel_weight[pix];
+      const bool on = m > 0.f;
+      ((i & 1) ? pw[i >> 1].y : pw[i >> 1].x) = on ? fminf(m, 1.f) : 0.f;
+      if (!on) nc[i] = 0;
+    }
+    mine = max(mine, nc[i]);
+  }
+  const uint32_t wm = __reduce_max_sync(0xffffffffu, mine);
+  if (lane == 0) s_wmax[warp] = wm;
+  if (threadIdx.x == 0) {
+    mbar_init(&s_bar[0], 1);
+    mbar_init(&s_bar[1], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  uint32_t maxc = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) maxc = max(maxc, s_wmax[w]);
+  int64_t used = end - start;
+  if ((int64_t)maxc < used) used = maxc;
+  const int nb = (int)((used + kBatch - 1) / kBatch);
+
+  // batch b uses buffer b & 1 and phase (b >> 1) & 1 of that buffer's barrier
+  int pend[2] = {-1, -1};  // batch whose copy into the buffer is in flight
+  bool clipped[2] = {false, false};
+  auto issue = [&](int b) {
+    if (stalled) return;
+    const int buf = b & 1;
+    const int64_t first = start + (int64_t)b * kBatch;
+    const int64_t rem = used - (int64_t)b * kBatch;
+    const int m = rem < kBatch ? (int)rem : kBatch;
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(&s_bar[buf], (uint32_t)(m * kRecBytes));
+    if ((int)threadIdx.x < m) {
+      uint32_t id = __ldg(&ids[first + threadIdx.x]);
+      clipped[buf] = id >= (uint32_t)geo.n;
+      if (clipped[buf]) {  // never read outside the records
+        id = 0;
+        atomicOr(status, kStatusBounds);
+      }
+      s_id[buf][threadIdx.x] = id;
+      bulk_copy_g2s(&s_rec[buf][threadIdx.x][0], rec_view + (size_t)id * GS_RECORD_FLOATS,
+                    kRecBytes, &s_bar[buf]);
+    }
+    pend[buf] = b;
+  };
+
+  const float pxc = (float)tp.px + 0.5f;
+  float2 pyc[NP];
+#pragma unroll
+  for (int q = 0; q < NP; ++q)
+    pyc[q] = make_float2((float)(tp.py + 8 * q) + 0.5f, (float)(tp.py + 8 * q) + 4.5f);
+  if (nb > 0) issue(0);
+  for (int b = 0; b < nb; ++b) {
+    const int buf = b & 1;
+    __syncthreads();  // previous batch fully consumed and flushed
+    if (b + 1 < nb) issue(b + 1);
+    const int64_t rem = used - (int64_t)b * kBatch;
+    const int m = rem < kBatch ? (int)rem : kBatch;
+    if (!__syncthreads_and(
+            mbar_wait_bounded(&s_bar[buf], (uint32_t)((b >> 1) & 1), wc.limit_ns, status)))
+      break;  // a copy did not land in time: give up on the tile
+    pend[buf] = -1;
+    if ((int)threadIdx.x < m) {
+      const uint32_t mask =
+          wmask_in ? (uint32_t)wmask_in[start + (int64_t)b * kBatch + threadIdx.x]
+                   : record_block_mask<NP>(&s_rec[buf][threadIdx.x][0], tp.x0, tp.y0);
+      s_mask[threadIdx.x] = clipped[buf] ? 0u : (uint8_t)mask;
+    }
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      s_sum[w][threadIdx.x] = 0.f;
+      s_max[w][threadIdx.x] = 0.f;
+    }
+    __syncthreads();
+    // this warp's pixels use no entry at or past the longest prefix among them
+    const int64_t wlim = (int64_t)wm - (int64_t)b * kBatch;
+    const int wc_n =
+        warp_list<NP>(s_mask, s_list[warp], wlim < m ? (wlim > 0 ? (int)wlim : 0) : m);
+    for (int k = 0; k < wc_n; ++k) {
+      const int j = s_list[warp][k];
+      const uint32_t pos = (uint32_t)(b * kBatch + j);
+      const float* r = &s_rec[buf][j][0];
+      float dx, a1, a2;
+      eval_col_s(r, pxc, dx, a1, a2);
+      float sum = 0.f, top = 0.f;
+#pragma unroll
+      for (int q = 0; q < NP; ++q) {
+        float2 dy, p1, p2;
+        const float2 zq = eval_zq_s(r, a1, a2, pyc[q], dy, p1, p2);
+        const bool o0 = pos < nc[2 * q] && zq.x <= 0.f;
+        const bool o1 = pos < nc[2 * q + 1] && zq.y <= 0.f;
+        const float2 a = make_float2(o0 ? fminf(kAlphaMax, alpha_raw_of(zq.x)) : 0.f,
+                                     o1 ? fminf(kAlphaMax, alpha_raw_of(zq.y)) : 0.f);
+        const float2 w = __fmul2_rn(pw[q], __fmul2_rn(a, T[q]));
+        T[q] = __fmul2_rn(T[q], __ffma2_rn(a, f2(-1.f), f2(1.f)));
+        sum += w.x + w.y;
+        top = fmaxf(top, fmaxf(w.x, w.y));
+      }
+      if (__ballot_sync(0xffffffffu, top > 0.f) == 0u) continue;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      }
+      if (lane == 0) {
+        s_sum[warp][j] = sum;
+        s_max[warp][j] = top;
+      }
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < m) {
+      float sum = 0.f, top = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        sum += s_sum[w][threadIdx.x];
+        top = fmaxf(top, s_max[w][threadIdx.x]);
+      }
+      if (sum > 0.f) {
+        const uint32_t id = s_id[buf][threadIdx.x];
+        atomicAdd(&sums[id], __float2ull_rn(sum * kWeightUnit));
+        if (largest) atomicMax(&largest[id], __float_as_uint(top));
+      }
+    }
+  }
+  // after a wait that gave up: copies still in flight land before the block
+  // exits
+#pragma unroll
+  for (int bf = 0; bf < 2; ++bf)
+    if (pend[bf] >= 0)
+      mbar_wait_bounded(&s_bar[bf], (uint32_t)((pend[bf] >> 1) & 1), wc.limit_ns, status);
+}
+
+// Before the walk: totals cleared, the kept maxima scaled (a decay of 0 reads
+// nothing). A kept maximum below zero or NaN counts as zero.
+__global__ void __launch_bounds__(256) k_weights_begin(unsigned long long* __restrict__ sums,
+                                                       float* __restrict__ largest, int n,
+                                                       float decay) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  sums[i] = 0ull;
+  if (largest) largest[i] = decay > 0.f ? fmaxf(decay * largest[i], 0.f) : 0.f;
+}
+
+// After the walk: sum <- decay sum + total, in double, rounded once.
+__global__ void __launch_bounds__(256) k_weights_end(const unsigned long long* __restrict__ sums,
+                                                     float* __restrict__ weight_sum, int n,
+                                                     float decay) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  const double t = (double)sums[i] * (1.0 / 4294967296.0);
+  weight_sum[i] = (float)(decay > 0.f ? fma((double)decay, (double)weight_sum[i], t) : t);
+}
+
 }  // namespace
 
 cudaError_t launch_raster_fwd(const float* records, const uint32_t* ids, const int64_t* ranges,
@@ -781,6 +989,24 @@ cudaError_t launch_raster_bwd(const float* records, const uint32_t* ids, const i
       records, ids, ranges, geo, bg[0], bg[1], bg[2], dL_dimage, final_T, n_contrib, warp_masks,
       grad2d,
       status, wc);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_blend_weights(const float* records, const uint32_t* ids, const int64_t* ranges,
+                                 int64_t capacity, const Grid& g, int n_views, int n,
+                                 const uint32_t* n_contrib, const uint8_t* warp_masks,
+                                 const float* pixel_weight, float decay, float* weight_sum,
+                                 float* weight_max, uint64_t* sums, uint32_t* status,
+                                 const WaitCfg& wc, cudaStream_t stream) {
+  const int64_t tiles = (int64_t)g.tiles_per_view * n_views;
+  const unsigned blocks = (unsigned)((n + 255) / 256);
+  unsigned long long* acc = reinterpret_cast<unsigned long long*>(sums);
+  k_weights_begin<<<blocks, 256, 0, stream>>>(acc, weight_max, n, decay);
+  RasterGeom geo{g, n, capacity};
+  k_blend_weights<kPairs><<<(unsigned)tiles, Shape<kPairs>::kThreads, 0, stream>>>(
+      records, ids, ranges, geo, n_contrib, warp_masks, pixel_weight, acc,
+      reinterpret_cast<uint32_t*>(weight_max), status, wc);
+  k_weights_end<<<blocks, 256, 0, stream>>>(acc, weight_sum, n, decay);
   return cudaGetLastError();
 }
 

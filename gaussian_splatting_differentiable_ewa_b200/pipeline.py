@@ -5,7 +5,8 @@ nothing else besides streams and the collectives of the multi-GPU step) and
 runs the calls in order: gs_project -> gs_bin_sort -> gs_rasterize_fwd ->
 [gs_l1_dssim against a target image] -> gs_rasterize_bwd -> gs_densify_stats
 -> gs_adam_step (or, with quantised SH, gs_adam_step_sh_quant for the SH), and
-gs_densify_and_prune when asked. Every step of the computation runs in
+gs_densify_and_prune when asked, or gs_blend_weights, gs_evict_select and
+gs_evict_compact to hold the set to a budget. Every step of the computation runs in
 libgs_b200.so.
 """
 
@@ -137,6 +138,8 @@ class Splatter:
         self.accum_plain = torch.zeros(n, dtype=f32, device=dev)
         self.accum_abs = torch.zeros(n, dtype=f32, device=dev)
         self.denom = torch.zeros(n, dtype=torch.int32, device=dev)
+        # accumulated blending weights, allocated by accumulate_weights
+        self.weight_sum = self.weight_max = self._weights_ws = None
         # with quantised SH the kernels read the codes themselves
         quant = self.sh_bits is not None
         self.c_params = api.params(self.means, self.log_scales, self.quats, self.opacity_logit,
@@ -327,6 +330,14 @@ class Splatter:
                 (self.accum_plain, self.accum_abs, self.denom), (self.m_flat, self.v_flat),
                 None if sh is None else (sh["lo"], sh["hi"]),
                 None if sh is None else sh["group"])
+
+    def _gather_for_evict(self, with_weights: bool) -> None:
+        """Before evict on several ranks: the summed blending weights and, when
+        the optimiser is sharded, every rank's slice of the moments."""
+        sh = self._shard
+        gdist.gather_for_densify(
+            (self.weight_sum,) if with_weights else (), (self.m_flat, self.v_flat),
+            None if sh is None else (sh["lo"], sh["hi"]), None if sh is None else sh["group"])
 
     def _graph_of(self, fn) -> "torch.cuda.CUDAGraph":
         """A CUDA graph of one fixed-shape call: run once outside capture (on
@@ -558,6 +569,26 @@ class Splatter:
                     self.image.copy_(imgs[1])
                 comp.wait_event(downloaded[(n - 1) & 1])
 
+    def _gather_sh_codes(self, codes: torch.Tensor, m: int):
+        """Quantised SH state of the m output Gaussians of the decisions
+        `codes` (gs_densify_sh_quant)."""
+        n, k3, dev = self.n, 3 * self.K, self.device
+        m_pad = -(-m // api.GS_QUANT_GROUP) * api.GS_QUANT_GROUP
+        state = (torch.zeros((k3, m_pad), device=dev, dtype=self.sh_codes.dtype),
+                 torch.zeros((k3, m_pad // api.GS_QUANT_GROUP, 2), dtype=torch.float32,
+                             device=dev),
+                 torch.zeros((k3, m_pad), dtype=torch.int16, device=dev),
+                 torch.zeros((k3, m_pad), dtype=torch.int16, device=dev))
+        q_out = api.sh_quant(state[0], state[1], m, k3, self.sh_bits)
+        ws2 = torch.zeros((api.gs_densify_sh_quant_workspace_size(n, m) + 255) // 256 * 256
+                          // 8, dtype=torch.int64, device=dev)
+        api.gs_densify_sh_quant(self.sh_q, self.sh_m16, self.sh_v16, codes, q_out, state[2],
+                                state[3], ws2, self.stream)
+        st = api.gs_get_status(ws2, self.stream)
+        if st != api.GS_OK:
+            raise api.GsError(st, "gs_densify_sh_quant")
+        return state
+
     def densify_and_prune(self, grad_threshold: float = 0.0002, scale_split: float = 0.05,
                           min_opacity: float = 0.005, max_scale: float = 1.0,
                           split_shrink: float = 1.6, use_abs: bool = True, z=None,
@@ -603,27 +634,98 @@ class Splatter:
         m = int(n_out.item())
         keep = lambda d: {k: d[k][:m] for k in d}  # noqa: E731
         o, mo, vo = keep(out), keep(m_out), keep(v_out)
-        sh_state = None
-        if quant:
-            k3 = 3 * self.K
-            m_pad = -(-m // api.GS_QUANT_GROUP) * api.GS_QUANT_GROUP
-            state = (torch.zeros((k3, m_pad), device=dev, dtype=self.sh_codes.dtype),
-                     torch.zeros((k3, m_pad // api.GS_QUANT_GROUP, 2), dtype=torch.float32,
-                                 device=dev),
-                     torch.zeros((k3, m_pad), dtype=torch.int16, device=dev),
-                     torch.zeros((k3, m_pad), dtype=torch.int16, device=dev))
-            q_out = api.sh_quant(state[0], state[1], m, k3, self.sh_bits)
-            ws2 = torch.zeros((api.gs_densify_sh_quant_workspace_size(n, m) + 255) // 256 * 256
-                              // 8, dtype=torch.int64, device=dev)
-            api.gs_densify_sh_quant(self.sh_q, self.sh_m16, self.sh_v16, codes, q_out, state[2],
-                                    state[3], ws2, self.stream)
-            st = api.gs_get_status(ws2, self.stream)
-            if st != api.GS_OK:
-                raise api.GsError(st, "gs_densify_sh_quant")
-            sh_state = state  # o["sh"] is not written: the decode of the new codes fills it
+        # with quantised SH o["sh"] is not written: the decode of the new codes fills it
+        sh_state = self._gather_sh_codes(codes, m) if quant else None
         self._alloc_gaussians(o["means"], o["log_scales"], o["quats"], o["opacity_logit"],
                               o["sh"], mo, vo, sh_state=sh_state)
         return codes[:n]
+
+    # ------------------------------------------------------------ eviction
+    def accumulate_weights(self, pixel_weight: Optional[torch.Tensor] = None,
+                           decay: float = 1.0, largest: bool = False) -> torch.Tensor:
+        """Add the blending weights of the frame just rendered (forward or
+        rasterize_fwd) to ``self.weight_sum``, scaled by `decay` first, and with
+        `largest` their maxima to ``self.weight_max`` (gs_blend_weights).
+        pixel_weight: float32 [V, H, W] in [0, 1], a mask or an error map.
+        Both start from zero and restart with every new Gaussian set."""
+        if pixel_weight is not None and (tuple(pixel_weight.shape) != (self.V, self.H, self.W)
+                                         or pixel_weight.dtype != torch.float32
+                                         or pixel_weight.device != self.ws.device
+                                         or not pixel_weight.is_contiguous()):
+            raise ValueError("pixel_weight must be contiguous float32 [V, H, W] on the device")
+        with self._torch_stream():
+            if self.weight_sum is None:
+                self.weight_sum = torch.zeros(self.n, dtype=torch.float32, device=self.device)
+                nb = api.gs_blend_weights_workspace_size(self.n)
+                self._weights_ws = torch.zeros(nb // 8, dtype=torch.int64, device=self.device)
+            if largest and self.weight_max is None:
+                self.weight_max = torch.zeros(self.n, dtype=torch.float32, device=self.device)
+        api.gs_blend_weights(self.c_proj, self.c_bins, self.cams, self.V, self.n, self.n_contrib,
+                             self.weight_sum, self._weights_ws,
+                             weight_max=self.weight_max if largest else None,
+                             warp_masks=self.warp_masks, pixel_weight=pixel_weight, decay=decay,
+                             stream=self.stream)
+        return self.weight_sum
+
+    def weights_status(self) -> int:
+        """Device conditions of accumulate_weights since the last query."""
+        return (api.GS_OK if self._weights_ws is None
+                else api.gs_get_status(self._weights_ws, self.stream))
+
+    def evict(self, n_keep: int, score: Optional[torch.Tensor] = None,
+              protect: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """Hold the set to n_keep Gaussians: those with the highest score
+        survive (``self.weight_sum`` when `score`, float32 [n], is None), the
+        ones marked in `protect` (uint8 or bool [n]) before all others, equal
+        scores by the lowest index (gs_evict_select). Parameters and moments
+        are compacted in index order (gs_evict_compact; quantised SH by
+        gs_densify_sh_quant), every per-Gaussian buffer is reallocated and the
+        statistics and weights restart from zero. On several ranks the
+        accumulated weights are summed first, so that every rank evicts
+        alike; a `score` or `protect` given must be the same on all of them.
+        Returns the decisions (int8 [n], 1 kept)."""
+        n, dev = self.n, self.device
+        n_keep = int(n_keep)
+        if n_keep < 1:
+            raise ValueError("n_keep must be at least 1")
+        if score is None and self.weight_sum is None:
+            raise ValueError("no score: call accumulate_weights first or give one")
+        if score is not None and (tuple(score.shape) != (n,) or score.dtype != torch.float32
+                                  or score.device != self.ws.device):
+            raise ValueError("score must be float32 [n] on the device")
+        if protect is not None and (tuple(protect.shape) != (n,)
+                                    or protect.dtype not in (torch.uint8, torch.bool)
+                                    or protect.device != self.ws.device):
+            raise ValueError("protect must be uint8 or bool [n] on the device")
+        quant = self.sh_bits is not None
+        names = [k for k, _ in self.param_list]
+        m = min(n, n_keep)
+        with self._torch_stream():
+            self._gather_for_evict(with_weights=score is None)
+            score = (self.weight_sum if score is None else score).contiguous()
+            protect = None if protect is None else protect.contiguous()
+
+            def like(t):
+                return torch.empty((m,) + tuple(t.shape[1:]), dtype=t.dtype, device=dev)
+
+            out = {k: like(t) for k, t in self.param_list}
+            m_out = {k: like(t) for k, t in self.param_list if not (quant and k == "sh")}
+            v_out = {k: like(t) for k, t in self.param_list if not (quant and k == "sh")}
+            grads_of = lambda d: api.grads(*[d.get(k) for k in names])  # noqa: E731
+            decisions = torch.empty(n, dtype=torch.int8, device=dev)
+            ws = torch.zeros(api.gs_evict_workspace_size(n) // 8, dtype=torch.int64, device=dev)
+            api.gs_evict_select(score, protect, n, n_keep, decisions, ws, self.stream)
+            api.gs_evict_compact(self.c_params, grads_of(self.exp_avg),
+                                 grads_of(self.exp_avg_sq), decisions, grads_of(out),
+                                 grads_of(m_out), grads_of(v_out), m, ws, stream=self.stream)
+            st = api.gs_get_status(ws, self.stream)
+            if st != api.GS_OK:
+                raise api.GsError(st, "gs_evict_compact")
+            sh_state = self._gather_sh_codes(decisions, m) if quant else None
+            self._alloc_gaussians(out["means"], out["log_scales"], out["quats"],
+                                  out["opacity_logit"], out["sh"], m_out, v_out,
+                                  sh_state=sh_state)
+        return decisions
 
     def status(self) -> int:
         return api.gs_get_status(self.ws, self.stream)

@@ -28,7 +28,8 @@
  *    never dereferenced), a Gaussian culled for non-finite values. The calls
  *    with a device wait or an index to check (gs_project, gs_bin_sort,
  *    gs_rasterize_fwd, gs_rasterize_bwd) take that workspace; the
- *    gs_bin_sort workspace serves all of them.
+ *    gs_bin_sort workspace serves all of them. gs_blend_weights and the
+ *    gs_evict_* calls have workspaces of their own, with the same word.
  *  - Pixel (x, y) has its centre at (x + 0.5, y + 0.5); tiles are 16 x 16
  *    pixels; tile index within a view is ty * tiles_x + tx, and the global
  *    tile index of view v is v * tiles_per_view + tile.
@@ -487,6 +488,79 @@ gs_status gs_densify_and_prune(const gs_params* in, const gs_grads* m_in, const 
                                gs_grads* v_out, int64_t out_capacity, int64_t* n_out,
                                int8_t* codes, void* ws, size_t ws_bytes, void* stream);
 
+/* ---- eviction under a budget -------------------------------------------
+ * A rendered pixel is a normalised weighting of its tile's list: the entry at
+ * position k has the weight w_k = alpha_k T_k (lshu.cn sec. 3.2 `blend`), and
+ * the weights and the background's T_final sum to one. Summed over pixels and
+ * views, a Gaussian's weights say how much the renders draw on it; holding
+ * the set to a budget evicts those that they draw on least. The pages only
+ * prune by opacity and scale; these calls hold a count. */
+
+/* Bytes of workspace gs_blend_weights needs for n Gaussians (256-byte
+ * aligned; the first 256 bytes hold the status word, zeroed once). */
+size_t gs_blend_weights_workspace_size(int64_t n);
+
+/* Accumulated blending weights of a rendered frame. With w_vpi the weight of
+ * Gaussian i at pixel p of view v (0 where it does not blend) and m the
+ * pixel's own weight, per Gaussian
+ *   weight_sum[i] <- decay weight_sum[i] + sum over v, p of m_vp w_vpi,
+ *   weight_max[i] <- max(decay weight_max[i], max over v, p of m_vp w_vpi).
+ * proj, bins, cams, n_views, n, n_contrib and warp_masks (NULL allowed) are
+ * those of the gs_rasterize_fwd call whose frame is meant; proj->bins,
+ * proj->radii and bins->n_pairs are not read.
+ *   pixel_weight  float [n_views][H][W] or NULL (every pixel counts 1): a
+ *                 mask or an error map in [0, 1]; a larger value counts 1, a
+ *                 negative one or NaN 0
+ *   decay         in [0, 1]; 0 overwrites both outputs without reading them
+ *   weight_sum    float [n]
+ *   weight_max    float [n], NULL skips it; a kept maximum below 0 or NaN
+ *                 counts as 0
+ * The sums of a call are held in 64-bit fixed point (units of 2^-32) and the
+ * step above is taken in double and rounded once, so results do not depend on
+ * the order in which tiles run: the same inputs give the same bits. Device
+ * conditions are those of gs_rasterize_fwd, in the status word of `ws`
+ * (gs_blend_weights_workspace_size(n) bytes; a tile whose batch copy timed out
+ * adds nothing further). GS_ERR_OVERFLOW when n_views H W exceeds 2^31. Three
+ * launches. */
+gs_status gs_blend_weights(const gs_projected* proj, const gs_binned* bins,
+                           const gs_camera* cams, int32_t n_views, int64_t n,
+                           const uint32_t* n_contrib, const uint8_t* warp_masks,
+                           const float* pixel_weight, float decay, float* weight_sum,
+                           float* weight_max, void* ws, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace gs_evict_select and gs_evict_compact need for n
+ * Gaussians (256-byte aligned; the first 256 bytes hold the status word,
+ * zeroed once). Either call leaves nothing the other one needs. */
+size_t gs_evict_workspace_size(int64_t n);
+
+/* Which Gaussians survive a budget of n_keep: decisions[i] (int8 [n]) becomes 1
+ * for the min(n, n_keep) that come first when ordered by
+ *   protected before unprotected (protect uint8 [n], nonzero = protected, e.g.
+ *     newborn Gaussians without a score yet; NULL: none),
+ *   then the higher score (float [n]; -0 equals 0, NaN below -infinity),
+ *   then the lower index,
+ * and 0 for the others. With more protected Gaussians than n_keep the lowest
+ * indices among them survive (their scores do not count). Exact: the
+ * threshold is an order statistic of the scores' bits. */
+gs_status gs_evict_select(const float* score, const uint8_t* protect, int64_t n, int64_t n_keep,
+                          int8_t* decisions, void* ws, size_t ws_bytes, void* stream);
+
+/* Compaction of the survivors (decisions[i] nonzero), in index order: the
+ * parameters to `out` and, unless all four moment arguments are NULL, the
+ * Adam moments to m_out and v_out (layouts of gs_params, out_capacity rows
+ * each, padding lanes copied). source, if not NULL, receives the input index
+ * of every output row (uint32 [out_capacity]), from which a caller gathers
+ * any other per-Gaussian array; *n_out (device int64, NULL skips it) the
+ * number of survivors. If they exceed out_capacity, the first out_capacity of
+ * them are written and GS_ERR_CAPACITY is raised in the status word. With
+ * quantised SH (in->sh_quant set) the sh fields of out and the moments may be
+ * NULL and are not touched: gs_densify_sh_quant builds the output's SH state
+ * from the same decisions (0 or 1). Outputs must not overlap inputs. */
+gs_status gs_evict_compact(const gs_params* in, const gs_grads* m_in, const gs_grads* v_in,
+                           const int8_t* decisions, gs_grads* out, gs_grads* m_out,
+                           gs_grads* v_out, int64_t out_capacity, uint32_t* source,
+                           int64_t* n_out, void* ws, size_t ws_bytes, void* stream);
+
 /* Bytes of workspace gs_l1_dssim needs for n_views views (sums and a block
  * counter; 8-byte aligned). */
 size_t gs_l1_dssim_workspace_size(int32_t n_views);
@@ -597,8 +671,9 @@ gs_status gs_densify_sh_quant(const gs_sh_quant* in, const uint16_t* m_in, const
  * finish. This call makes one such wait run out on purpose, without faulting
  * anything:
  *   GS_STALL_RASTER_FWD / GS_STALL_RASTER_BWD  global tile `index` of the
- *     next rasteriser calls issues no record copies and waits in vain for
- *     its first batch (its pixels keep the background / add no gradient);
+ *     next rasteriser calls (gs_blend_weights follows the former) issues no record copies and waits in vain for
+ *     its first batch (its pixels keep the background / add no gradient or
+ *     weight);
  *   GS_STALL_EMIT_LOOKBACK  emission block `index` of gs_bin_sort's
  *     look-back scan (GS_SORT_FULL64, and GS_SORT_PRESORT on grids that
  *     sort by tile id) never publishes its prefix, so its successors' waits

@@ -623,3 +623,84 @@ def adam_sh_quant(codes, bounds, grad_sh, m16, v16, n: int, bits: int, lr: float
     x[:, :n] = p.astype(np.float32)
     c, b = quantize_groups(x, n, bits, rounding, seed, step)
     return c, b, m_out, v_out, p
+
+
+# --------------------------------------------------------------- eviction
+
+def blend_weights(records, ids, ranges, n_contrib, width: int, height: int, pixel_weight=None):
+    """Accumulated blending weights of one call, float64, tile by tile and entry
+    by entry: per Gaussian the sum and the maximum over views and pixels of
+    m alpha T, alpha = min(0.99, 2^-zq / 255) where zq <= 0, over the list
+    prefix n_contrib of each pixel; m the pixel weight clamped to [0, 1], NaN
+    as 0.
+
+    records [V, n, 16] float32; ids, ranges the binned lists; n_contrib
+    [V, H, W]. Returns (sum [n], max [n], slack [n]): |sum of a float32 walk -
+    sum| <= slack when that walk takes dx, dy, the fma chains a_i, p_i, zq, 2^x
+    with relative error 2^-22, one product for alpha, T (1 - alpha) per entry
+    and sums of at most 12 roundings per term (u = 2^-24): with the errors of
+    dx (u), the product and sum of a_i (u |a_i|), dy (u) and p_i (u |p_i|),
+      dp_i = u (|w_ix dx| + |a_i| + |w_iy dy| + |p_i|),
+      dzq  = sum 2 |p_i| dp_i + dp_i^2 + u (|t| + |zq|),
+      alpha is off by ln 2 dzq + 2^-22 + 4u relative, T by alpha / (1 - alpha)
+      times that plus 2u per entry; an entry with |zq| <= dzq may be taken or
+      skipped: T m / 255 on its own weight, 1/254 relative on T after it.
+    """
+    u = 2.0 ** -24
+    rec = np.asarray(records, np.float64)
+    V, n = rec.shape[:2]
+    tx, ty = -(-width // 16), -(-height // 16)
+    total, top, slack = np.zeros(n), np.zeros(n), np.zeros(n)
+    lane = np.arange(256)
+    for t, (a, b) in enumerate(np.asarray(ranges)):
+        v, tt = divmod(t, tx * ty)
+        x, y = (tt % tx) * 16 + lane % 16, (tt // tx) * 16 + lane // 16
+        ok = (x < width) & (y < height)
+        xi, yi = np.minimum(x, width - 1), np.minimum(y, height - 1)
+        nc = np.where(ok, np.asarray(n_contrib)[v, yi, xi], 0)
+        m = np.ones(256)
+        if pixel_weight is not None:
+            pw = np.asarray(pixel_weight, np.float64)[v, yi, xi]
+            m = np.where(np.isnan(pw), 0.0, np.clip(pw, 0.0, 1.0))
+        T, eT = np.ones(256), np.zeros(256)
+        for k in range(min(int(nc.max(initial=0)), int(b - a))):
+            i = int(ids[a + k])
+            r = rec[v, i]
+            dx, dy = x + 0.5 - r[0], y + 0.5 - r[1]
+            zq, dz = r[8], 0.0
+            for wx, wy, c in ((r[2], r[3], r[4]), (r[5], r[6], r[7])):
+                ai = wx * dx + c
+                p = ai + wy * dy
+                dp = u * (np.abs(wx * dx) + np.abs(ai) + np.abs(wy * dy) + np.abs(p))
+                zq = zq + p * p
+                dz = dz + 2 * np.abs(p) * dp + dp * dp + u * np.abs(zq)
+            dz = dz * (1 + 2.0 ** -10)  # second-order terms
+            live = k < nc
+            take = live & (zq <= 0)
+            near = live & (np.abs(zq) <= dz)
+            al = np.where(take, np.minimum(0.99, np.exp2(-np.minimum(zq, 8.0)) / 255.0), 0.0)
+            ea = np.where(take, np.log(2.0) * dz + 2.0 ** -22 + 4 * u, 0.0)
+            w = al * T * m
+            total[i] += w.sum()
+            top[i] = max(top[i], w.max())
+            slack[i] += (w * (ea + eT + 12 * u)).sum() + (near * T * m).sum() * 1.01 / 255.0
+            T = T * (1.0 - al)
+            eT = eT + al / (1.0 - al) * ea + 2 * u + near / 254.0
+    return total, top, slack
+
+
+def evict_select(score, protect, n_keep: int) -> np.ndarray:
+    """1 for the n_keep Gaussians that come first by (protected, higher score,
+    lower index), NaN scores last, by sorting tuples."""
+    s = [float(x) for x in np.asarray(score)]
+    n = len(s)
+    prot = [False] * n if protect is None else [bool(p) for p in protect]
+
+    def key(i):
+        if prot[i]:
+            return (0, 0, 0.0, i)
+        return (1, 1, 0.0, i) if s[i] != s[i] else (1, 0, -s[i], i)
+
+    out = np.zeros(n, np.int8)
+    out[sorted(range(n), key=key)[:n_keep]] = 1
+    return out
