@@ -664,7 +664,7 @@ gs_status gs_blend_weights(const gs_projected* proj, const gs_binned* bins, cons
   return cuda_status(launch_blend_weights(
       proj->records, bins->ids, bins->ranges, bins->pair_capacity, g, n_views, (int)n, n_contrib,
       warp_masks, pixel_weight, decay, weight_sum, weight_max, sums, status_word(ws),
-      wait_cfg(GS_STALL_RASTER_FWD), static_cast<cudaStream_t>(stream)));
+      static_cast<cudaStream_t>(stream)));
 }
 
 namespace {

@@ -139,7 +139,7 @@ cudaError_t launch_blend_weights(const float* records, const uint32_t* ids, cons
                                  const uint32_t* n_contrib, const uint8_t* warp_masks,
                                  const float* pixel_weight, float decay, float* weight_sum,
                                  float* weight_max, uint64_t* sums, uint32_t* status,
-                                 const WaitCfg& wc, cudaStream_t stream);
+                                 cudaStream_t stream);
 cudaError_t launch_densify(const float* grad2d, const int* radii, int n_views, int n,
                            float* accum_plain, float* accum_abs, int* denom, cudaStream_t stream);
 cudaError_t launch_adam(const gs_adam_group* groups, int n_groups, float b1, float b2, float eps,

@@ -517,11 +517,12 @@ size_t gs_blend_weights_workspace_size(int64_t n);
  *                 counts as 0
  * The sums of a call are held in 64-bit fixed point (units of 2^-32) and the
  * step above is taken in double and rounded once, so results do not depend on
- * the order in which tiles run: the same inputs give the same bits. Device
- * conditions are those of gs_rasterize_fwd, in the status word of `ws`
- * (gs_blend_weights_workspace_size(n) bytes; a tile whose batch copy timed out
- * adds nothing further). GS_ERR_OVERFLOW when n_views H W exceeds 2^31. Three
- * launches. */
+ * the order in which tiles run: the same inputs give the same bits. The status
+ * word of `ws` (gs_blend_weights_workspace_size(n) bytes) receives
+ * GS_STATUS_BIT_BOUNDS for an entry it has to read that names a Gaussian >= n
+ * (the entry adds nothing) or a tile range outside the ids buffer (the tile
+ * adds nothing); nothing waits on the device. GS_ERR_OVERFLOW when n_views H W
+ * exceeds 2^31. Three launches. */
 gs_status gs_blend_weights(const gs_projected* proj, const gs_binned* bins,
                            const gs_camera* cams, int32_t n_views, int64_t n,
                            const uint32_t* n_contrib, const uint8_t* warp_masks,
@@ -671,9 +672,8 @@ gs_status gs_densify_sh_quant(const gs_sh_quant* in, const uint16_t* m_in, const
  * finish. This call makes one such wait run out on purpose, without faulting
  * anything:
  *   GS_STALL_RASTER_FWD / GS_STALL_RASTER_BWD  global tile `index` of the
- *     next rasteriser calls (gs_blend_weights follows the former) issues no record copies and waits in vain for
- *     its first batch (its pixels keep the background / add no gradient or
- *     weight);
+ *     next rasteriser calls issues no record copies and waits in vain for
+ *     its first batch (its pixels keep the background / add no gradient);
  *   GS_STALL_EMIT_LOOKBACK  emission block `index` of gs_bin_sort's
  *     look-back scan (GS_SORT_FULL64, and GS_SORT_PRESORT on grids that
  *     sort by tile id) never publishes its prefix, so its successors' waits

@@ -3,8 +3,8 @@ the same records and lists (and against the rasteriser's own backward), the
 survivors against a sort of tuples, the compaction against indexing.
 
 Bars. weight_sum: |gpu - float64| <= slack, the walk's own error bound
-(oracle.blend_weights), plus the fixed-point rounding (2^-33 per tile) and the
-last rounding (2^-24 relative, of the decayed sum too). weight_max: within the
+(oracle.blend_weights), plus the fixed-point rounding (2^-33 for each of a
+tile's four 8 x 8 blocks) and the last rounding (2^-24 relative, of the decayed sum too). weight_max: within the
 same slack. Decisions, sources and rows: equal."""
 
 import numpy as np
@@ -90,7 +90,7 @@ def test_weights_match_the_float64_walk(name, kw, masks, weighted, decay):
     assert api.gs_get_status(ws) == api.GS_OK
     tiles = sp.ranges.shape[0]
     exp = np.float64(np.float32(decay)) * old + want
-    tol = slack + tiles * 2.0 ** -33 + U * exp
+    tol = slack + 4 * tiles * 2.0 ** -33 + U * exp
     assert np.all(np.abs(total.cpu().numpy() - exp) <= tol)
     exp_top = np.maximum(np.float64(np.float32(decay)) * old_top, want_top)
     assert np.all(np.abs(top.cpu().numpy() - exp_top) <= slack + 2 * U * exp_top)
@@ -165,9 +165,10 @@ def test_empty_frames_and_single_sides():
         assert not s.any() and not t.any()
 
 
-def test_weights_conditions_are_reported():
+@pytest.mark.parametrize("masks", [True, False])
+def test_weights_conditions_are_reported(masks):
     """A list entry naming no Gaussian and a range past the ids are clipped and
-    reported; a tile that waits in vain ends in time and adds nothing."""
+    reported, with the forward's masks and without."""
     sp = _frame("fwd_1k_128")
     want, _, ws = _weights(sp)
     ids, ranges = sp.ids.clone(), sp.ranges.clone()
@@ -176,7 +177,8 @@ def test_weights_conditions_are_reported():
     s = torch.zeros(sp.n, device="cuda")
 
     def call(b):
-        api.gs_blend_weights(sp.c_proj, b, sp.cams, sp.V, sp.n, sp.n_contrib, s, ws, decay=0.0)
+        api.gs_blend_weights(sp.c_proj, b, sp.cams, sp.V, sp.n, sp.n_contrib, s, ws, decay=0.0,
+                             warp_masks=sp.warp_masks if masks else None)
         return api.gs_get_status(ws)
 
     first = int(ranges[busy, 0])
@@ -191,13 +193,6 @@ def test_weights_conditions_are_reported():
     assert call(bins) == api.GS_ERR_OVERFLOW
     assert float(s.sum()) < float(want.sum())
     ranges[busy, 1] = sp.ranges[busy, 1]
-    assert call(bins) == api.GS_OK and torch.equal(s, want)
-    try:
-        api.gs_debug_stall(api.GS_STALL_RASTER_FWD, busy, 0.05)
-        assert call(bins) == api.GS_ERR_DEVICE_TIMEOUT
-    finally:
-        api.gs_debug_stall(api.GS_STALL_NONE)
-    assert 0 < float(s.sum()) < float(want.sum())
     assert call(bins) == api.GS_OK and torch.equal(s, want)
 
 
