@@ -683,7 +683,7 @@ gsb::EvictScratch evict_scratch(void* ws, int64_t n) {
 size_t gs_evict_workspace_size(int64_t n) {
   if (n < 0 || n >= (1ll << 31)) return 0;
   return align_up(kControlBytes + sizeof(gsb::EvictState) +
-                  (size_t)(gsb::evict_groups(n) + gsb::evict_blocks(n)) * sizeof(uint32_t));
+                  (size_t)(gsb::evict_groups(n) + gsb::evict_counts(n)) * sizeof(uint32_t));
 }
 
 gs_status gs_evict_select(const float* score, const uint8_t* protect, int64_t n, int64_t n_keep,
@@ -695,7 +695,8 @@ gs_status gs_evict_select(const float* score, const uint8_t* protect, int64_t n,
   if (!score || !decisions || !aligned(score, 4)) return GS_ERR_INVALID_ARG;
   return cuda_status(gsb::launch_evict_select(score, protect, (int)n,
                                               (int)(n_keep < n ? n_keep : n), decisions,
-                                              evict_scratch(ws, n),
+                                              evict_scratch(ws, n), status_word(ws),
+                                              wait_cfg(GS_STALL_SORT_LOOKBACK),
                                               static_cast<cudaStream_t>(stream)));
 }
 

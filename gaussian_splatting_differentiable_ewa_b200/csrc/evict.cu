@@ -5,22 +5,25 @@
 // blending weights, or any score), protected ones first, equal scores by the
 // lowest index. A score becomes a 32-bit key whose unsigned order is the
 // score's; the threshold is the n_keep-th largest key, found digit by digit
-// (11 + 11 + 10 bits) from counts alone:
+// from counts alone. Of the keys equal to the threshold the first ones in
+// index order survive. One launch either way:
 //
-//  k_ev_digit   counts one digit of the keys that share the digits found so
-//               far; the block that finishes last finds the digit of the
-//               n_keep-th key.
-//  k_ev_equal   keys equal to the threshold per block (nothing to do when all
-//               of them survive).
-//  k_ev_write   decisions: keys above the threshold, and the first of the equal
-//               ones in index order.
+//  k_ev_select       small sets: one block, the keys in its registers, four
+//                    digits of 8 bits.
+//  k_ev_select_grid  larger sets: up to one block per SM, launched together;
+//                    the keys are read again for every digit (11 + 11 + 10
+//                    bits; from L2 up to some 25M Gaussians) and the counts
+//                    meet in global memory, behind a grid barrier with a time
+//                    limit.
 //
 // Compaction moves the survivors' rows in index order:
 //
-//  k_ev_count   survivors per block.
-//  k_ev_move    every block adds up the counts before it, lists its survivors
-//               and copies their rows; consecutive threads write consecutive
-//               elements of the output.
+//  k_ev_count   survivors per 256 Gaussians (and per 1024 of those).
+//  k_ev_move    every block adds up the survivors before its 256 Gaussians --
+//               from the counts, or for small sets from the decisions
+//               themselves -- lists its own and copies their rows of one
+//               array set (parameters, first or second moments); consecutive
+//               threads write consecutive elements of the output.
 
 #include <cuda_runtime.h>
 
@@ -29,22 +32,23 @@
 namespace gsb {
 namespace {
 
-constexpr int kEvThreads = 256;
-constexpr int kEvRows = 1024;  // Gaussians per block of the index-ordered kernels
-constexpr int kEvPer = kEvRows / kEvThreads;
-constexpr int kEvGroup = 1024;  // blocks per group total
-
 // Key of a score: unsigned order = score order, -0 and +0 alike, NaN the
 // lowest (0), a protected Gaussian the highest (above +infinity).
-__device__ __forceinline__ uint32_t ev_key(const float* score, const uint8_t* protect, int i) {
-  if (protect && protect[i]) return 0xffffffffu;
-  const uint32_t b = __float_as_uint(score[i]);
-  if ((b & 0x7fffffffu) > 0x7f800000u) return 0u;
-  if (b == 0x80000000u) return 0x80000000u;
-  return (b >> 31) ? ~b : (b | 0x80000000u);
+__device__ __forceinline__ uint32_t ev_key(float score, bool prot) {
+  const uint32_t b = __float_as_uint(score);
+  uint32_t key = (b >> 31) ? ~b : (b | 0x80000000u);
+  if (b == 0x80000000u) key = 0x80000000u;
+  if ((b & 0x7fffffffu) > 0x7f800000u) key = 0u;
+  return prot ? 0xffffffffu : key;
+}
+
+__device__ __forceinline__ uint32_t ev_key_at(const float* score, const uint8_t* protect,
+                                              int64_t i) {
+  return ev_key(__ldg(&score[i]), protect && protect[i]);
 }
 
 // Exclusive sum over the block's threads of x, and the total.
+template <int WARPS>
 __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* s_w, uint32_t& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t incl = x;
@@ -56,239 +60,587 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* s_w, uint32
   __syncthreads();
   if (lane == 31) s_w[warp] = incl;
   __syncthreads();
-  uint32_t before = 0;
-  total = 0;
+  uint32_t w = lane < WARPS ? s_w[lane] : 0u, wi = w;
 #pragma unroll
-  for (int w = 0; w < kEvThreads / 32; ++w) {
-    before += w < warp ? s_w[w] : 0u;
-    total += s_w[w];
+  for (int o = 1; o < WARPS; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, wi, o);
+    if (lane >= o) wi += y;
   }
-  return before + incl - x;
+  total = __shfl_sync(0xffffffffu, wi, WARPS - 1);
+  return __shfl_sync(0xffffffffu, wi - w, warp) + incl - x;
 }
 
-// Sum of the counts of the blocks before this one, by the whole block: whole
-// groups of kEvGroup blocks from their group totals, the rest one by one.
-__device__ __forceinline__ uint32_t counts_before(const uint32_t* counts, const uint32_t* groups,
-                                                  uint32_t* s_w) {
-  const unsigned g = blockIdx.x / kEvGroup;
-  uint32_t s = 0, total;
-  for (unsigned b = threadIdx.x; b < g; b += kEvThreads) s += groups[b];
-  for (unsigned b = g * kEvGroup + threadIdx.x; b < blockIdx.x; b += kEvThreads) s += counts[b];
-  block_scan(s, s_w, total);
-  return total;
-}
-
-template <int PASS>
-__global__ void __launch_bounds__(kEvThreads) k_ev_digit(const float* __restrict__ score,
-                                                         const uint8_t* __restrict__ protect,
-                                                         int n, int n_keep, EvictState* st) {
-  constexpr int kShift = PASS == 0 ? 21 : (PASS == 1 ? 10 : 0);
-  constexpr uint32_t kBins = PASS == 2 ? 1024 : 2048;
-  __shared__ uint32_t s_hist[kBins];
-  __shared__ uint32_t s_w[kEvThreads / 32];
-  __shared__ bool s_last;
-  for (uint32_t d = threadIdx.x; d < kBins; d += kEvThreads) s_hist[d] = 0;
-  __syncthreads();
-  const uint32_t prefix = PASS == 0 ? 0u : st->prefix;
-  for (int64_t i = (int64_t)blockIdx.x * kEvThreads + threadIdx.x; i < n;
-       i += (int64_t)gridDim.x * kEvThreads) {
-    const uint32_t key = ev_key(score, protect, (int)i);
-    constexpr int kHigh = PASS == 0 ? 0 : (PASS == 1 ? 21 : 10);
-    if (PASS == 0 || (key >> kHigh) == (prefix >> kHigh))
-      atomicAdd(&s_hist[(key >> kShift) & (kBins - 1)], 1u);
-  }
-  __syncthreads();
-  for (uint32_t d = threadIdx.x; d < kBins; d += kEvThreads)
-    if (s_hist[d]) atomicAdd(&st->hist[PASS][d], s_hist[d]);
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) s_last = atomicAdd(&st->done[PASS], 1u) == gridDim.x - 1;
-  __syncthreads();
-  if (!s_last) return;
-  // the last block: from the highest digit down, the one in which the wanted
-  // key lies
-  __threadfence();
-  const uint32_t want = PASS == 0 ? (uint32_t)n_keep : st->rank;
-  constexpr uint32_t kPer = kBins / kEvThreads;
-  uint32_t c[kPer], sum = 0, total;
+// From the highest digit down, the one in which the wanted key lies: thread t
+// holds the counts of bins BINS - 1 - (t PER + k) (0 past the last bin). One
+// thread finds it and writes the digit, the rank left within it and its count.
+template <int WARPS, uint32_t BINS, int PER>
+__device__ __forceinline__ void find_digit(const uint32_t (&c)[PER], uint32_t want, uint32_t* s_w,
+                                           uint32_t* found) {
+  uint32_t sum = 0, total;
 #pragma unroll
-  for (uint32_t k = 0; k < kPer; ++k) {
-    c[k] = __ldcg(&st->hist[PASS][kBins - 1 - (threadIdx.x * kPer + k)]);
-    sum += c[k];
-  }
-  uint32_t above = block_scan(sum, s_w, total);
+  for (int k = 0; k < PER; ++k) sum += c[k];
+  uint32_t above = block_scan<WARPS>(sum, s_w, total);
 #pragma unroll
-  for (uint32_t k = 0; k < kPer; ++k) {
+  for (int k = 0; k < PER; ++k) {
     if (above < want && want <= above + c[k]) {
-      st->prefix = prefix | ((kBins - 1 - (threadIdx.x * kPer + k)) << kShift);
-      st->rank = want - above;
-      if (PASS == 2) st->equal = c[k];
+      found[0] = BINS - 1 - (threadIdx.x * PER + k);
+      found[1] = want - above;
+      found[2] = c[k];
     }
     above += c[k];
   }
 }
 
-__global__ void __launch_bounds__(kEvThreads) k_ev_equal(const float* __restrict__ score,
-                                                         const uint8_t* __restrict__ protect,
-                                                         int n, const EvictState* st,
-                                                         uint32_t* __restrict__ counts,
-                                                         uint32_t* __restrict__ groups) {
-  __shared__ uint32_t s_w[kEvThreads / 32];
-  if (st->equal == st->rank) return;
-  const uint32_t t = st->prefix;
-  uint32_t x = 0, total;
-#pragma unroll
-  for (int k = 0; k < kEvPer; ++k) {
-    const int64_t i = (int64_t)blockIdx.x * kEvRows + k * kEvThreads + threadIdx.x;
-    if (i < n) x += ev_key(score, protect, (int)i) == t;
-  }
-  block_scan(x, s_w, total);
-  if (threadIdx.x == 0) {
-    counts[blockIdx.x] = total;
-    if (total) atomicAdd(&groups[blockIdx.x / kEvGroup], total);
-  }
-}
+// ------------------------------------------------------------ selection, small
 
-__global__ void __launch_bounds__(kEvThreads) k_ev_write(const float* __restrict__ score,
-                                                         const uint8_t* __restrict__ protect,
-                                                         int n, const EvictState* st,
-                                                         const uint32_t* __restrict__ counts,
-                                                         const uint32_t* __restrict__ groups,
-                                                         int8_t* __restrict__ decisions) {
-  __shared__ uint32_t s_w[kEvThreads / 32];
-  const uint32_t t = st->prefix, rank = st->rank;
-  const bool ties = st->equal != rank;
-  uint32_t before = ties ? counts_before(counts, groups, s_w) : 0u;
-  for (int k = 0; k < kEvPer; ++k) {
-    const int64_t i = (int64_t)blockIdx.x * kEvRows + k * kEvThreads + threadIdx.x;
-    const uint32_t key = i < n ? ev_key(score, protect, (int)i) : 0u;
-    bool keep = key > t || (key == t && !ties);
-    if (ties) {
-      uint32_t total;
-      const bool eq = i < n && key == t;
-      const uint32_t e = before + block_scan(eq, s_w, total);
-      keep = keep || (eq && e < rank);
-      before += total;
+constexpr int kSelThreads = 1024;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelKeys = 8;  // keys per thread, in registers
+constexpr int kSelMax = kSelThreads * kSelKeys;
+
+// The warps hold consecutive spans of 32 per_thread Gaussians; lane l of a
+// warp its elements l, l + 32, ... Digit counts have one counter per lane:
+// equal scores by the thousand (Gaussians never seen), or scores of one
+// magnitude, would otherwise make a warp's 32 additions wait for one another.
+__global__ void __launch_bounds__(kSelThreads) k_ev_select(const float* __restrict__ score,
+                                                           const uint8_t* __restrict__ protect,
+                                                           int n, int n_keep, int per_thread,
+                                                           int8_t* __restrict__ decisions) {
+  __shared__ uint4 s_copies[256][8];  // [digit][32 lanes]
+  __shared__ __align__(16) uint32_t s_hist[256];
+  __shared__ uint32_t s_equal[kSelWarps];
+  __shared__ uint32_t s_found[3];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int first = warp * 32 * per_thread + lane;
+  int mine = first < n ? (n - first + 31) / 32 : 0;  // elements this lane holds
+  if (mine > per_thread) mine = per_thread;
+  uint32_t key[kSelKeys];
+#pragma unroll
+  for (int k = 0; k < kSelKeys; ++k) {
+    if (k >= per_thread) break;
+    key[k] = k < mine ? ev_key_at(score, protect, first + 32 * k) : 0u;
+  }
+  (&s_copies[0][0])[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+  (&s_copies[0][0])[threadIdx.x + kSelThreads] = make_uint4(0u, 0u, 0u, 0u);
+  __syncthreads();
+
+  uint32_t t = 0, rank = (uint32_t)n_keep, equal = 0;
+  uint32_t* copies = reinterpret_cast<uint32_t*>(s_copies) + lane;
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    const uint32_t known = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
+#pragma unroll
+    for (int k = 0; k < kSelKeys; ++k) {
+      if (k >= per_thread) break;
+      if (k < mine && ((key[k] ^ t) & known) == 0u)
+        atomicAdd(&copies[((key[k] >> shift) & 255u) * 32], 1u);
     }
-    if (i < n) decisions[i] = keep ? 1 : 0;
-  }
-}
-
-__global__ void __launch_bounds__(kEvThreads) k_ev_count(const int8_t* __restrict__ decisions,
-                                                         int n, uint32_t* __restrict__ counts,
-                                                         uint32_t* __restrict__ groups) {
-  __shared__ uint32_t s_w[kEvThreads / 32];
-  uint32_t x = 0, total;
+    __syncthreads();
+    // four threads to a digit; the counters are cleared for the next one
+    uint4* c = &s_copies[threadIdx.x >> 2][2 * (threadIdx.x & 3)];
+    const uint4 a = c[0], b = c[1];
+    c[0] = c[1] = make_uint4(0u, 0u, 0u, 0u);
+    uint32_t x = a.x + a.y + a.z + a.w + b.x + b.y + b.z + b.w;
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    x += __shfl_xor_sync(0xffffffffu, x, 2);
+    if ((threadIdx.x & 3) == 0) s_hist[threadIdx.x >> 2] = x;
+    __syncthreads();
+    // the first warp, eight digits to a lane from the highest down, finds the
+    // one in which the wanted key lies
+    if (warp == 0) {
+      const uint4 hi = *reinterpret_cast<const uint4*>(&s_hist[252 - 8 * lane]);
+      const uint4 lo = *reinterpret_cast<const uint4*>(&s_hist[248 - 8 * lane]);
+      const uint32_t h[8] = {hi.w, hi.z, hi.y, hi.x, lo.w, lo.z, lo.y, lo.x};
+      uint32_t sum = 0;
 #pragma unroll
-  for (int k = 0; k < kEvPer; ++k) {
-    const int64_t i = (int64_t)blockIdx.x * kEvRows + k * kEvThreads + threadIdx.x;
-    if (i < n) x += decisions[i] != 0;
+      for (int k = 0; k < 8; ++k) sum += h[k];
+      uint32_t incl = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      uint32_t above = incl - sum;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (above < rank && rank <= above + h[k]) {
+          s_found[0] = 255 - (8 * lane + k);
+          s_found[1] = rank - above;
+          s_found[2] = h[k];
+        }
+        above += h[k];
+      }
+    }
+    __syncthreads();
+    t |= s_found[0] << shift;
+    rank = s_found[1];
+    equal = s_found[2];
   }
-  block_scan(x, s_w, total);
+
+  // equal keys before this warp's, when not all of them survive
+  const bool ties = equal != rank;
+  uint32_t before = 0;
+  if (ties) {
+    uint32_t e = 0;
+#pragma unroll
+    for (int k = 0; k < kSelKeys; ++k) {
+      if (k >= per_thread) break;
+      e += __popc(__ballot_sync(0xffffffffu, k < mine && key[k] == t));
+    }
+    if (lane == 0) s_equal[warp] = e;
+    __syncthreads();
+    before = __reduce_add_sync(0xffffffffu, lane < warp ? s_equal[lane] : 0u);
+  }
+  const uint32_t lt = lanemask_lt();
+#pragma unroll
+  for (int k = 0; k < kSelKeys; ++k) {
+    if (k >= per_thread) break;
+    const bool eq = k < mine && key[k] == t;
+    bool keep = k < mine && key[k] >= t;
+    if (ties) {
+      const uint32_t bal = __ballot_sync(0xffffffffu, eq);
+      keep = keep && (!eq || before + __popc(bal & lt) < rank);
+      before += __popc(bal);
+    }
+    if (k < mine) decisions[first + 32 * k] = keep ? 1 : 0;
+  }
+}
+
+// ------------------------------------------------------------ selection, large
+
+constexpr int kGridFlight = 2;                        // 16-byte reads in flight per thread
+constexpr int kWarpFlight = 2;                        // the same where warps go by themselves
+constexpr int kCopies = 4;                            // counters per digit, by lane
+constexpr int kGridMin = kSelThreads;                 // Gaussians per block at least
+constexpr uint32_t kZeroKey = 0x80000000u;            // the key of a score of 0
+
+// Digit PASS of a key, the most significant first, and the bits above it.
+template <int PASS>
+struct Digit {
+  static constexpr int kShift = PASS == 0 ? 21 : (PASS == 1 ? 10 : 0);
+  static constexpr uint32_t kBins = PASS == 2 ? 1024 : 2048;
+  __device__ static bool shares(uint32_t key, uint32_t prefix) {
+    constexpr int kHigh = PASS == 0 ? 31 : (PASS == 1 ? 21 : 10);
+    return PASS == 0 || (key >> kHigh) == (prefix >> kHigh);
+  }
+  __device__ static uint32_t of(uint32_t key) { return (key >> kShift) & (kBins - 1); }
+};
+
+// Keys of Gaussians i .. i + 3, by one 16-byte and one 4-byte read where VEC
+// says the pointers allow it. Scores that are neither negative nor NaN and
+// unprotected, as accumulated weights mostly are, take the short way: this
+// kernel is bound by its instructions per key.
+template <bool VEC>
+__device__ __forceinline__ void ev_keys4(const float* __restrict__ score,
+                                         const uint8_t* __restrict__ protect, int64_t i,
+                                         uint32_t (&key)[4]) {
+  uint32_t b[4], p = 0;
+  if (VEC) {
+    const uint4 f = __ldg(reinterpret_cast<const uint4*>(score + i));
+    b[0] = f.x, b[1] = f.y, b[2] = f.z, b[3] = f.w;
+    if (protect) p = __ldg(reinterpret_cast<const uint32_t*>(protect + i));
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      b[k] = __float_as_uint(__ldg(&score[i + k]));
+      if (protect && protect[i + k]) p |= 0xffu << (8 * k);
+    }
+  }
+  if (max(max(b[0], b[1]), max(b[2], b[3])) <= 0x7f800000u && p == 0u) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) key[k] = b[k] | 0x80000000u;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) key[k] = ev_key(__uint_as_float(b[k]), (p >> (8 * k)) & 0xffu);
+  }
+}
+
+// Barrier over the grid, number `turn` of the launch (from 1): false when the
+// other blocks did not arrive within the limit.
+__device__ __forceinline__ bool grid_barrier(uint32_t* arrived, uint32_t turn, bool* s_ok,
+                                             const WaitCfg& wc, uint32_t* status) {
+  __syncthreads();
   if (threadIdx.x == 0) {
-    counts[blockIdx.x] = total;
-    if (total) atomicAdd(&groups[blockIdx.x / kEvGroup], total);
-  }
-}
-
-struct EvArray {
-  const void* in;
-  void* out;
-  int per;   // elements per row
-  int wide;  // 16-byte elements (else 4-byte)
-};
-struct EvArrays {
-  EvArray a[15];
-  int n;
-};
-
-template <typename E>
-__device__ __forceinline__ void move_rows(const EvArray& a, const uint16_t* s_row, int64_t first,
-                                          int64_t base, uint32_t m) {
-  const E* in = static_cast<const E*>(a.in) + first * a.per;
-  E* out = static_cast<E*>(a.out) + base * a.per;
-  const uint32_t total = m * a.per;
-#pragma unroll 4
-  for (uint32_t e = threadIdx.x; e < total; e += kEvThreads) {
-    const uint32_t r = e / a.per, q = e - r * a.per;
-    out[e] = __ldg(in + (uint32_t)s_row[r] * a.per + q);
-  }
-}
-
-__global__ void __launch_bounds__(kEvThreads) k_ev_move(EvArrays arrays,
-                                                        const int8_t* __restrict__ decisions,
-                                                        int n, int64_t capacity,
-                                                        const uint32_t* __restrict__ counts,
-                                                        const uint32_t* __restrict__ groups,
-                                                        uint32_t* __restrict__ source,
-                                                        int64_t* __restrict__ n_out,
-                                                        uint32_t* __restrict__ status) {
-  __shared__ uint32_t s_w[kEvThreads / 32];
-  __shared__ uint16_t s_row[kEvRows];
-  const int64_t base = counts_before(counts, groups, s_w);
-  const int64_t first = (int64_t)blockIdx.x * kEvRows;
-  uint32_t m = 0;
-  for (int k = 0; k < kEvPer; ++k) {
-    const int r = k * kEvThreads + threadIdx.x;
-    const bool keep = first + r < n && decisions[first + r] != 0;
-    uint32_t total;
-    const uint32_t o = m + block_scan(keep, s_w, total);
-    if (keep) s_row[o] = (uint16_t)r;
-    m += total;
+    __threadfence();
+    // test hook: this block never arrives
+    if ((int64_t)blockIdx.x != wc.stall) atomicAdd(arrived, 1u);
+    const uint32_t want = turn * gridDim.x;
+    const uint64_t t0 = globaltimer_ns();
+    bool ok;
+    while (!(ok = *reinterpret_cast<volatile uint32_t*>(arrived) >= want))
+      if (globaltimer_ns() - t0 > wc.limit_ns) break;
+    if (!ok) atomicOr(status, kStatusTimeout);
+    __threadfence();
+    *s_ok = ok;
   }
   __syncthreads();
-  if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) {
+  return *s_ok;
+}
+
+struct GridShared {
+  uint4 copies[2048];
+  uint32_t w[kSelWarps];
+  uint32_t found[3];
+  bool ok;
+};
+
+// One digit of the wanted key over the block's Gaussians [first, end), then
+// over the grid. False: gave up at the barrier.
+template <int PASS, bool VEC>
+__device__ __forceinline__ bool grid_digit(GridShared& s, const float* __restrict__ score,
+                                           const uint8_t* __restrict__ protect, int64_t first,
+                                           int64_t end, EvictState* st, uint32_t& prefix,
+                                           uint32_t& want, uint32_t& equal, const WaitCfg& wc,
+                                           uint32_t* status) {
+  using D = Digit<PASS>;
+  static_assert(kCopies * sizeof(uint32_t) == sizeof(uint4), "one uint4 per digit");
+  uint32_t* copies = reinterpret_cast<uint32_t*>(s.copies) + (threadIdx.x & (kCopies - 1));
+  for (uint32_t d = threadIdx.x; d < D::kBins; d += kSelThreads)
+    s.copies[d] = make_uint4(0u, 0u, 0u, 0u);
+  __syncthreads();
+  // Gaussians never seen have a score of exactly 0: those are counted in
+  // registers, they would queue up at one counter
+  uint32_t zeros = 0;
+  auto count = [&](uint32_t key) {
+    if (key == kZeroKey)
+      ++zeros;
+    else if (D::shares(key, prefix))
+      atomicAdd(&copies[D::of(key) * kCopies], 1u);
+  };
+  const int64_t whole = first + ((end - first) & ~(int64_t)3);
+  for (int64_t i = first + 4 * threadIdx.x; i < whole; i += 4 * kSelThreads * kGridFlight) {
+    uint32_t key[kGridFlight][4];
+#pragma unroll
+    for (int f = 0; f < kGridFlight; ++f)
+      if (i + 4 * kSelThreads * f < whole)
+        ev_keys4<VEC>(score, protect, i + 4 * kSelThreads * f, key[f]);
+#pragma unroll
+    for (int f = 0; f < kGridFlight; ++f) {
+      if (i + 4 * kSelThreads * f >= whole) continue;
+      // four keys at once that all differ from the wanted one above this digit
+      if (PASS > 0 && min(min(key[f][0] - prefix, key[f][1] - prefix),
+                          min(key[f][2] - prefix, key[f][3] - prefix)) >= D::kBins << D::kShift)
+        continue;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) count(key[f][k]);
+    }
+  }
+  if (whole + threadIdx.x < end) count(ev_key_at(score, protect, whole + threadIdx.x));
+  zeros = __reduce_add_sync(0xffffffffu, zeros);
+  if ((threadIdx.x & 31) == 0 && zeros && D::shares(kZeroKey, prefix))
+    atomicAdd(&copies[D::of(kZeroKey) * kCopies], zeros);
+  __syncthreads();
+  for (uint32_t d = threadIdx.x; d < D::kBins; d += kSelThreads) {
+    const uint4 h = s.copies[d];
+    const uint32_t c = h.x + h.y + h.z + h.w;
+    if (c) atomicAdd(&st->hist[PASS][d], c);
+  }
+  if (!grid_barrier(&st->arrived, PASS + 1, &s.ok, wc, status)) return false;
+  constexpr int kPer = D::kBins / kSelThreads;
+  uint32_t c[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k)
+    c[k] = __ldcg(&st->hist[PASS][D::kBins - 1 - (threadIdx.x * kPer + k)]);
+  find_digit<kSelWarps, D::kBins, kPer>(c, want, s.w, s.found);
+  __syncthreads();
+  prefix |= s.found[0] << D::kShift;
+  want = s.found[1];
+  equal = s.found[2];
+  return true;
+}
+
+template <bool VEC>
+__device__ __forceinline__ void put_decisions(int8_t* d, bool a, bool b, bool c, bool e) {
+  if (VEC) {
+    *reinterpret_cast<uint32_t*>(d) =
+        (a ? 1u : 0u) | (b ? 1u << 8 : 0u) | (c ? 1u << 16 : 0u) | (e ? 1u << 24 : 0u);
+  } else {
+    d[0] = a, d[1] = b, d[2] = c, d[3] = e;
+  }
+}
+
+// Every block holds a contiguous share of the set (a multiple of 4).
+template <bool VEC>
+__global__ void __launch_bounds__(kSelThreads) k_ev_select_grid(
+    const float* __restrict__ score, const uint8_t* __restrict__ protect, int n, int n_keep,
+    int64_t share, EvictState* st, uint32_t* counts, int8_t* __restrict__ decisions, WaitCfg wc,
+    uint32_t* status) {
+  __shared__ GridShared s;
+  const int64_t first = blockIdx.x * share < n ? blockIdx.x * share : n;
+  const int64_t end = first + share < n ? first + share : n;
+  uint32_t t = 0, rank = (uint32_t)n_keep, equal = 0;
+  if (!grid_digit<0, VEC>(s, score, protect, first, end, st, t, rank, equal, wc, status) ||
+      !grid_digit<1, VEC>(s, score, protect, first, end, st, t, rank, equal, wc, status) ||
+      !grid_digit<2, VEC>(s, score, protect, first, end, st, t, rank, equal, wc, status))
+    return;
+
+  // the decisions, a warp over a contiguous part of the block's share, so that
+  // ties need no more than the equal keys before each warp
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t part = ((end - first + 4 * kSelWarps - 1) / (4 * kSelWarps)) * 4;
+  const int64_t w0 = first + warp * part < end ? first + warp * part : end;
+  const int64_t w1 = w0 + part < end ? w0 + part : end;
+  const int64_t whole = w0 + ((w1 - w0) & ~(int64_t)3);  // then up to three single ones
+  const bool single = whole + lane < w1;
+  if (equal == rank) {
+    for (int64_t i = w0 + 4 * lane; i < whole; i += 128 * kWarpFlight) {
+      uint32_t key[kWarpFlight][4];
+#pragma unroll
+      for (int f = 0; f < kWarpFlight; ++f)
+        if (i + 128 * f < whole) ev_keys4<VEC>(score, protect, i + 128 * f, key[f]);
+#pragma unroll
+      for (int f = 0; f < kWarpFlight; ++f)
+        if (i + 128 * f < whole)
+          put_decisions<VEC>(decisions + i + 128 * f, key[f][0] >= t, key[f][1] >= t,
+                             key[f][2] >= t, key[f][3] >= t);
+    }
+    if (single) decisions[whole + lane] = ev_key_at(score, protect, whole + lane) >= t ? 1 : 0;
+    return;
+  }
+
+  // not all of the equal keys survive: those before this warp's
+  uint32_t x = 0, total, before;
+  for (int64_t i = w0 + 4 * lane; i < whole; i += 128 * kWarpFlight) {
+    uint32_t key[kWarpFlight][4];
+#pragma unroll
+    for (int f = 0; f < kWarpFlight; ++f)
+      if (i + 128 * f < whole) ev_keys4<VEC>(score, protect, i + 128 * f, key[f]);
+#pragma unroll
+    for (int f = 0; f < kWarpFlight; ++f)
+      if (i + 128 * f < whole) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x += key[f][k] == t;
+      }
+  }
+  if (single) x += ev_key_at(score, protect, whole + lane) == t;
+  x = __reduce_add_sync(0xffffffffu, x);
+  const uint32_t in_block =
+      __shfl_sync(0xffffffffu, block_scan<kSelWarps>(lane == 0 ? x : 0u, s.w, total), 0);
+  if (threadIdx.x == 0) counts[blockIdx.x] = total;
+  if (!grid_barrier(&st->arrived, 4, &s.ok, wc, status)) return;
+  uint32_t y = 0;
+  for (unsigned b = threadIdx.x; b < blockIdx.x; b += kSelThreads) y += __ldcg(&counts[b]);
+  block_scan<kSelWarps>(y, s.w, before);
+  before += in_block;
+  for (int64_t i0 = w0; i0 < whole; i0 += 128 * kWarpFlight) {
+    uint32_t key[kWarpFlight][4];
+#pragma unroll
+    for (int f = 0; f < kWarpFlight; ++f) {
+      key[f][0] = key[f][1] = key[f][2] = key[f][3] = ~t;  // a lane past the end: not equal
+      if (i0 + 128 * f + 4 * lane < whole)
+        ev_keys4<VEC>(score, protect, i0 + 128 * f + 4 * lane, key[f]);
+    }
+#pragma unroll
+    for (int f = 0; f < kWarpFlight; ++f) {
+      uint32_t eq = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) eq += key[f][k] == t;
+      uint32_t incl = eq;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t z = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += z;
+      }
+      uint32_t e = before + incl - eq;
+      before += __shfl_sync(0xffffffffu, incl, 31);
+      bool keep[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        keep[k] = key[f][k] > t || (key[f][k] == t && e < rank);
+        e += key[f][k] == t;
+      }
+      if (i0 + 128 * f + 4 * lane < whole)
+        put_decisions<VEC>(decisions + i0 + 128 * f + 4 * lane, keep[0], keep[1], keep[2],
+                           keep[3]);
+    }
+  }
+  const uint32_t key = single ? ev_key_at(score, protect, whole + lane) : ~t;
+  const uint32_t e = before + __popc(__ballot_sync(0xffffffffu, key == t) & lanemask_lt());
+  if (single) decisions[whole + lane] = key > t || (key == t && e < rank) ? 1 : 0;
+}
+
+// ------------------------------------------------------------ compaction
+
+constexpr int kMoveRows = 256;     // Gaussians (and threads) per block
+constexpr int kMoveGroup = 1024;   // blocks per group total
+constexpr int kMoveDirect = 32768; // up to here blocks read the decisions before theirs
+
+// Nonzero bytes of a word.
+__device__ __forceinline__ uint32_t nonzero_bytes(uint32_t x) {
+  return __popc((((x & 0x7f7f7f7fu) + 0x7f7f7f7fu) | x) & 0x80808080u);
+}
+
+// Survivors among decisions[a .. b), added up by `threads` threads of which
+// this is number t (their parts, not the total).
+__device__ __forceinline__ uint32_t survivors_part(const int8_t* __restrict__ decisions, int64_t a,
+                                                   int64_t b, int t, int threads) {
+  uint32_t x = 0;
+  if ((reinterpret_cast<uintptr_t>(decisions) & 7) == 0 && (a & 7) == 0) {
+    for (int64_t i = a + 8 * t; i < b; i += 8 * (int64_t)threads) {
+      if (i + 7 < b) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(decisions + i));
+        x += nonzero_bytes(w.x) + nonzero_bytes(w.y);
+      } else {
+        for (int64_t j = i; j < b; ++j) x += decisions[j] != 0;
+      }
+    }
+  } else {
+    for (int64_t i = a + t; i < b; i += threads) x += decisions[i] != 0;
+  }
+  return x;
+}
+
+// Eight lanes per kMoveRows Gaussians, 32 of those per block.
+__global__ void __launch_bounds__(256) k_ev_count(const int8_t* __restrict__ decisions, int n,
+                                                  int blocks, uint32_t* __restrict__ counts,
+                                                  uint32_t* __restrict__ groups) {
+  __shared__ uint32_t s_w[8];
+  const int b = blockIdx.x * 32 + (threadIdx.x >> 3), lane = threadIdx.x & 7;
+  const int64_t a = (int64_t)b * kMoveRows, e = a + kMoveRows < n ? a + kMoveRows : n;
+  uint32_t x = b < blocks ? survivors_part(decisions, a, e, lane, 8) : 0u, total;
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  if (lane == 0 && b < blocks) counts[b] = x;
+  if (!groups) return;
+  block_scan<8>(lane == 0 ? x : 0u, s_w, total);
+  if (threadIdx.x == 0 && total) atomicAdd(&groups[blockIdx.x * 32 / kMoveGroup], total);
+}
+
+// One array set: the fields of gs_params.
+struct EvSet {
+  const float4 *means, *log_scales, *quats;
+  const float *logit, *sh;
+  float4 *o_means, *o_log_scales, *o_quats;
+  float *o_logit, *o_sh;
+};
+struct EvSets {
+  EvSet s[3];
+};
+
+// SH rows of PER elements of type E (kNoSh: none).
+constexpr int kNoSh = -1;
+template <typename E, int PER>
+__global__ void __launch_bounds__(kMoveRows) k_ev_move(EvSets sets,
+                                                       const int8_t* __restrict__ decisions,
+                                                       int n, int64_t capacity,
+                                                       const uint32_t* __restrict__ counts,
+                                                       const uint32_t* __restrict__ groups,
+                                                       uint32_t* __restrict__ source,
+                                                       int64_t* __restrict__ n_out,
+                                                       uint32_t* __restrict__ status) {
+  constexpr int kWarps = kMoveRows / 32;
+  __shared__ uint32_t s_w[kWarps];
+  __shared__ uint8_t s_row[kMoveRows];
+  const int64_t first = (int64_t)blockIdx.x * kMoveRows;
+  // survivors before this block
+  uint32_t part = 0, before;
+  if (counts) {
+    const unsigned g = groups ? blockIdx.x / kMoveGroup : 0u;
+    for (unsigned b = threadIdx.x; b < g; b += kMoveRows) part += groups[b];
+    for (unsigned b = g * kMoveGroup + threadIdx.x; b < blockIdx.x; b += kMoveRows)
+      part += counts[b];
+  } else {
+    part = survivors_part(decisions, 0, first, threadIdx.x, kMoveRows);
+  }
+  const bool keep = first + threadIdx.x < n && decisions[first + threadIdx.x] != 0;
+  block_scan<kWarps>(part, s_w, before);
+  uint32_t m;
+  const uint32_t o = block_scan<kWarps>(keep ? 1u : 0u, s_w, m);
+  const int64_t base = before;
+  if (keep) s_row[o] = (uint8_t)threadIdx.x;
+  __syncthreads();
+  if (blockIdx.x == gridDim.x - 1 && blockIdx.y == 0 && threadIdx.x == 0) {
     *n_out = base + m;
     if (base + m > capacity) atomicOr(status, kStatusCapacity);
   }
   // rows past the capacity are not written
   if (base + m > capacity) m = base < capacity ? (uint32_t)(capacity - base) : 0u;
-  if (source)
-    for (uint32_t r = threadIdx.x; r < m; r += kEvThreads)
-      source[base + r] = (uint32_t)(first + s_row[r]);
-  for (int k = 0; k < arrays.n; ++k) {
-    if (arrays.a[k].wide)
-      move_rows<float4>(arrays.a[k], s_row, first, base, m);
-    else
-      move_rows<float>(arrays.a[k], s_row, first, base, m);
+
+  const EvSet& s = sets.s[blockIdx.y];
+  if (threadIdx.x < m) {
+    const int64_t i = first + s_row[threadIdx.x], j = base + threadIdx.x;
+    const float4 a = __ldg(&s.means[i]), b = __ldg(&s.log_scales[i]), c = __ldg(&s.quats[i]);
+    const float d = __ldg(&s.logit[i]);
+    s.o_means[j] = a;
+    s.o_log_scales[j] = b;
+    s.o_quats[j] = c;
+    s.o_logit[j] = d;
+    if (source && blockIdx.y == 0) source[j] = (uint32_t)i;
+  }
+  if constexpr (PER > 0) {
+    const E* in = reinterpret_cast<const E*>(s.sh) + first * PER;
+    E* out = reinterpret_cast<E*>(s.o_sh) + base * PER;
+    const uint32_t total = m * PER;
+    constexpr int kFlight = 6;  // reads in flight per thread
+    for (uint32_t e0 = threadIdx.x; e0 < total; e0 += kFlight * kMoveRows) {
+      E v[kFlight];
+#pragma unroll
+      for (int k = 0; k < kFlight; ++k) {
+        const uint32_t e = e0 + k * kMoveRows, r = e / PER;
+        if (e < total) v[k] = __ldg(in + (uint32_t)s_row[r] * PER + (e - r * PER));
+      }
+#pragma unroll
+      for (int k = 0; k < kFlight; ++k) {
+        const uint32_t e = e0 + k * kMoveRows;
+        if (e < total) out[e] = v[k];
+      }
+    }
   }
 }
 
-void add_arrays(EvArrays& v, const DpTensorPtrs& in, const DpTensorPtrs& out, int k3) {
-  if (!in.means) return;
-  v.a[v.n++] = EvArray{in.means, out.means, 1, 1};
-  v.a[v.n++] = EvArray{in.log_scales, out.log_scales, 1, 1};
-  v.a[v.n++] = EvArray{in.quats, out.quats, 1, 1};
-  v.a[v.n++] = EvArray{in.logit, out.logit, 1, 0};
-  if (k3 > 0) {
-    const bool wide = k3 % 4 == 0;
-    v.a[v.n++] = EvArray{in.sh, out.sh, wide ? k3 / 4 : k3, wide};
-  }
+EvSet ev_set(const DpTensorPtrs& in, const DpTensorPtrs& out) {
+  auto c4 = [](const float* p) { return reinterpret_cast<const float4*>(p); };
+  auto m4 = [](float* p) { return reinterpret_cast<float4*>(p); };
+  return EvSet{c4(in.means),  c4(in.log_scales),  c4(in.quats),  in.logit,  in.sh,
+               m4(out.means), m4(out.log_scales), m4(out.quats), out.logit, out.sh};
 }
+
+int move_blocks(int64_t n) { return (int)((n + kMoveRows - 1) / kMoveRows); }
+
+constexpr int kMaxSms = 1024;  // room for the counts of one block per SM
 
 }  // namespace
 
-int64_t evict_blocks(int64_t n) { return (n + kEvRows - 1) / kEvRows; }
-int64_t evict_groups(int64_t n) { return (evict_blocks(n) + kEvGroup - 1) / kEvGroup; }
+int64_t evict_groups(int64_t n) { return (move_blocks(n) + kMoveGroup - 1) / kMoveGroup; }
+int64_t evict_counts(int64_t n) {
+  return move_blocks(n) > kMaxSms ? move_blocks(n) : kMaxSms;
+}
 
 cudaError_t launch_evict_select(const float* score, const uint8_t* protect, int n, int n_keep,
-                                int8_t* decisions, const EvictScratch& w, cudaStream_t stream) {
+                                int8_t* decisions, const EvictScratch& w, uint32_t* status,
+                                const WaitCfg& wc, cudaStream_t stream) {
   if (n == 0) return cudaSuccess;
   if (n_keep <= 0 || n_keep >= n)
     return cudaMemsetAsync(decisions, n_keep > 0 ? 1 : 0, (size_t)n, stream);
-  // the group totals follow the state
-  const cudaError_t e =
-      cudaMemsetAsync(w.state, 0, sizeof(EvictState) + (size_t)evict_groups(n) * 4, stream);
+  if (n <= kSelMax) {
+    k_ev_select<<<1, kSelThreads, 0, stream>>>(score, protect, n, n_keep,
+                                               (n + kSelThreads - 1) / kSelThreads, decisions);
+    return cudaGetLastError();
+  }
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess)
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = cudaMemsetAsync(w.state, 0, sizeof(EvictState), stream);
   if (e != cudaSuccess) return e;
-  const int nb = (int)evict_blocks(n);
-  const int db = nb < 592 ? nb : 592;
-  k_ev_digit<0><<<db, kEvThreads, 0, stream>>>(score, protect, n, n_keep, w.state);
-  k_ev_digit<1><<<db, kEvThreads, 0, stream>>>(score, protect, n, n_keep, w.state);
-  k_ev_digit<2><<<db, kEvThreads, 0, stream>>>(score, protect, n, n_keep, w.state);
-  k_ev_equal<<<nb, kEvThreads, 0, stream>>>(score, protect, n, w.state, w.counts, w.groups);
-  k_ev_write<<<nb, kEvThreads, 0, stream>>>(score, protect, n, w.state, w.counts, w.groups,
-                                            decisions);
-  return cudaGetLastError();
+  if (sms > kMaxSms) sms = kMaxSms;
+  // one block per SM, or one for every kGridMin Gaussians
+  const int64_t want = ((int64_t)n + kGridMin - 1) / kGridMin;
+  const int blocks = want < sms ? (int)want : sms;
+  const int64_t share = ((int64_t)n + 4 * (int64_t)blocks - 1) / (4 * (int64_t)blocks) * 4;
+  const bool vec = (reinterpret_cast<uintptr_t>(score) & 15) == 0 &&
+                   (reinterpret_cast<uintptr_t>(protect) & 3) == 0 &&
+                   (reinterpret_cast<uintptr_t>(decisions) & 3) == 0;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr{};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  attr.id = cudaLaunchAttributeCooperative;  // all blocks at once, or an error
+  attr.val.cooperative = 1;
+  return cudaLaunchKernelEx(&cfg, vec ? k_ev_select_grid<true> : k_ev_select_grid<false>, score,
+                            protect, n, n_keep, share, w.state, w.counts, decisions, wc, status);
 }
 
 cudaError_t launch_evict_compact(const DpTensorPtrs& p_in, const DpTensorPtrs& m_in,
@@ -298,16 +650,30 @@ cudaError_t launch_evict_compact(const DpTensorPtrs& p_in, const DpTensorPtrs& m
                                  int64_t* n_out, const EvictScratch& w, uint32_t* status,
                                  cudaStream_t stream) {
   if (n == 0) return cudaMemsetAsync(n_out, 0, sizeof(int64_t), stream);
-  EvArrays v{};
-  add_arrays(v, p_in, p_out, k3);
-  add_arrays(v, m_in, m_out, k3);
-  add_arrays(v, v_in, v_out, k3);
-  const cudaError_t e = cudaMemsetAsync(w.groups, 0, (size_t)evict_groups(n) * 4, stream);
-  if (e != cudaSuccess) return e;
-  const int nb = (int)evict_blocks(n);
-  k_ev_count<<<nb, kEvThreads, 0, stream>>>(decisions, n, w.counts, w.groups);
-  k_ev_move<<<nb, kEvThreads, 0, stream>>>(v, decisions, n, capacity, w.counts, w.groups, source,
-                                           n_out, status);
+  const int nb = move_blocks(n);
+  uint32_t *counts = nullptr, *groups = nullptr;
+  if (n > kMoveDirect) {
+    counts = w.counts;
+    if (nb > kMoveGroup) {
+      groups = w.groups;
+      const cudaError_t e =
+          cudaMemsetAsync(groups, 0, (size_t)evict_groups(n) * sizeof(uint32_t), stream);
+      if (e != cudaSuccess) return e;
+    }
+    k_ev_count<<<(nb + 31) / 32, 256, 0, stream>>>(decisions, n, nb, counts, groups);
+  }
+  EvSets sets{};
+  sets.s[0] = ev_set(p_in, p_out);
+  sets.s[1] = ev_set(m_in, m_out);
+  sets.s[2] = ev_set(v_in, v_out);
+  const dim3 grid(nb, m_in.means ? 3 : 1);
+  const auto move = k3 == 48   ? k_ev_move<float4, 12>
+                    : k3 == 27 ? k_ev_move<float, 27>
+                    : k3 == 12 ? k_ev_move<float4, 3>
+                    : k3 == 3  ? k_ev_move<float, 3>
+                               : k_ev_move<float, kNoSh>;
+  move<<<grid, kMoveRows, 0, stream>>>(sets, decisions, n, capacity, counts, groups, source, n_out,
+                                       status);
   return cudaGetLastError();
 }
 

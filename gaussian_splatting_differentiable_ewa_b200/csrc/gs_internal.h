@@ -181,22 +181,20 @@ cudaError_t launch_densify_and_prune(const DpTensorPtrs& p_in, const DpTensorPtr
 
 // Eviction under a budget (evict.cu).
 struct EvictState {
-  uint32_t hist[3][2048];  // key digits of each pass, the most significant first
-  uint32_t done[3];        // blocks that finished a pass
-  uint32_t prefix;         // key digits found so far: the threshold key at the end
-  uint32_t rank;           // survivors still to come from the keys that share them
-  uint32_t equal;          // keys equal to the threshold
-  uint32_t reserved[2];
+  uint32_t hist[3][2048];  // key digits, the most significant first
+  uint32_t arrived;        // blocks that came to the grid barrier, all turns
+  uint32_t reserved[7];
 };
 struct EvictScratch {
   EvictState* state;
-  uint32_t* groups;  // [evict_groups(n)], right behind the state
-  uint32_t* counts;  // [evict_blocks(n)]
+  uint32_t* groups;  // [evict_groups(n)]
+  uint32_t* counts;  // [evict_counts(n)]
 };
-int64_t evict_blocks(int64_t n);
 int64_t evict_groups(int64_t n);
+int64_t evict_counts(int64_t n);
 cudaError_t launch_evict_select(const float* score, const uint8_t* protect, int n, int n_keep,
-                                int8_t* decisions, const EvictScratch& w, cudaStream_t stream);
+                                int8_t* decisions, const EvictScratch& w, uint32_t* status,
+                                const WaitCfg& wc, cudaStream_t stream);
 // m_in / v_in with NULL arrays: no moments. k3 0: no SH.
 cudaError_t launch_evict_compact(const DpTensorPtrs& p_in, const DpTensorPtrs& m_in,
                                  const DpTensorPtrs& v_in, const int8_t* decisions, int n, int k3,

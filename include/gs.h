@@ -542,7 +542,10 @@ size_t gs_evict_workspace_size(int64_t n);
  *   then the lower index,
  * and 0 for the others. With more protected Gaussians than n_keep the lowest
  * indices among them survive (their scores do not count). Exact: the
- * threshold is an order statistic of the scores' bits. */
+ * threshold is an order statistic of the scores' bits. One launch; above
+ * 131,072 Gaussians its blocks, one per SM, run together and wait for one
+ * another: GS_STATUS_BIT_TIMEOUT when that took too long (the decisions are
+ * then not all written). */
 gs_status gs_evict_select(const float* score, const uint8_t* protect, int64_t n, int64_t n_keep,
                           int8_t* decisions, void* ws, size_t ws_bytes, void* stream);
 
@@ -667,7 +670,8 @@ gs_status gs_densify_sh_quant(const gs_sh_quant* in, const uint16_t* m_in, const
 
 /* Test hook for the timeout path (the pages have no counterpart). Every
  * device-side wait of the library (an mbarrier phase in gs_project and the
- * rasteriser, a look-back flag in gs_bin_sort's emission and radix passes)
+ * rasteriser, a look-back flag in gs_bin_sort's emission and radix passes, the
+ * grid barrier of gs_evict_select)
  * gives up after a time limit, sets GS_STATUS_BIT_TIMEOUT and lets its kernel
  * finish. This call makes one such wait run out on purpose, without faulting
  * anything:
@@ -682,6 +686,8 @@ gs_status gs_densify_sh_quant(const gs_sh_quant* in, const uint16_t* m_in, const
  *     single-sweep radix passes (the depth keys of GS_SORT_PRESORT, the pair
  *     keys of GS_SORT_FULL64) publishes neither its digit counts nor its
  *     prefix in any pass, so the waits of the partitions after it run out;
+ *     in gs_evict_select above 131,072 Gaussians, block `index` never comes
+ *     to the barrier of the launch;
  *   GS_STALL_NONE  back to normal.
  * wait_limit_s (> 0) replaces the default limit of 2 s for every wait while
  * the setting holds; 0 keeps the default. Process-wide, not thread-safe

@@ -236,19 +236,49 @@ def test_survivors_match_the_sorted_order(n, kind):
     assert api.gs_get_status(ws) == api.GS_OK
 
 
-@pytest.mark.parametrize("n,keep", [(3_000_001, 1_000_003), (2_097_152, 2_097_151)])
-def test_survivors_of_large_sets_with_ties(n, keep):
+@pytest.mark.parametrize("off", [0, 1])
+@pytest.mark.parametrize("n,keep", [(131_072, 70_000), (131_073, 131_072), (200_003, 1),
+                                    (3_000_001, 1_000_003), (2_097_152, 2_097_151)])
+def test_survivors_of_large_sets_with_ties(n, keep, off):
     """Equal scores by the million at the threshold: the lowest indices, across
-    every block and group of blocks."""
+    blocks, on aligned and on odd addresses."""
     g = torch.Generator(device="cuda").manual_seed(n)
-    score = torch.rand(n, generator=g, device="cuda")
+    score = torch.rand(n + off, generator=g, device="cuda")[off:]
     score[torch.rand(n, generator=g, device="cuda") < 0.8] = 0.0
-    d = torch.empty(n, dtype=torch.int8, device="cuda")
-    api.gs_evict_select(score, None, n, keep, d, _ws(api.gs_evict_workspace_size(n)))
+    protect = (torch.rand(n + off, generator=g, device="cuda") < 0.1).to(torch.uint8)[off:]
+    d = torch.empty(n + off, dtype=torch.int8, device="cuda")[off:]
+    ws = _ws(api.gs_evict_workspace_size(n))
+    for p in (None, protect):
+        api.gs_evict_select(score, p, n, keep, d, ws)
+        s = score if p is None else torch.where(p != 0, torch.inf, score)
+        best = torch.sort(s, descending=True, stable=True).indices[:keep]
+        want = torch.zeros_like(d)
+        want[best] = 1
+        assert torch.equal(d, want)
+    assert api.gs_get_status(ws) == api.GS_OK
     best = torch.sort(score, descending=True, stable=True).indices[:keep]
+    api.gs_evict_select(score, None, n, keep, d, ws)
     want = torch.zeros_like(d)
     want[best] = 1
     assert torch.equal(d, want)
+
+
+def test_selection_that_waits_in_vain_is_reported():
+    """A block of the large selection that never comes to the barrier: the
+    others give up in time, and the next call is normal."""
+    n = 300_000
+    score = torch.arange(n, dtype=torch.float32, device="cuda")
+    d = torch.empty(n, dtype=torch.int8, device="cuda")
+    ws = _ws(api.gs_evict_workspace_size(n))
+    try:
+        api.gs_debug_stall(api.GS_STALL_SORT_LOOKBACK, 5, 0.05)
+        api.gs_evict_select(score, None, n, n // 2, d, ws)
+        assert api.gs_get_status(ws) == api.GS_ERR_DEVICE_TIMEOUT
+    finally:
+        api.gs_debug_stall(api.GS_STALL_NONE)
+    api.gs_evict_select(score, None, n, n // 2, d, ws)
+    assert api.gs_get_status(ws) == api.GS_OK
+    assert not d[:n // 2].any() and torch.all(d[n // 2:] == 1)
 
 
 def _sets(n, K, count, seed=0):
