@@ -493,6 +493,7 @@ __device__ __forceinline__ uint32_t survivors_part(const int8_t* __restrict__ de
 __global__ void __launch_bounds__(256) k_ev_count(const int8_t* __restrict__ decisions, int n,
                                                   int blocks, uint32_t* __restrict__ counts,
                                                   uint32_t* __restrict__ groups) {
+  let_next_begin();
   __shared__ uint32_t s_w[8];
   const int b = blockIdx.x * 32 + (threadIdx.x >> 3), lane = threadIdx.x & 7;
   const int64_t a = (int64_t)b * kMoveRows, e = a + kMoveRows < n ? a + kMoveRows : n;
@@ -522,8 +523,8 @@ template <typename E, int PER>
 __global__ void __launch_bounds__(kMoveRows) k_ev_move(EvSets sets,
                                                        const int8_t* __restrict__ decisions,
                                                        int n, int64_t capacity,
-                                                       const uint32_t* __restrict__ counts,
-                                                       const uint32_t* __restrict__ groups,
+                                                       const uint32_t* counts,
+                                                       const uint32_t* groups,
                                                        uint32_t* __restrict__ source,
                                                        int64_t* __restrict__ n_out,
                                                        uint32_t* __restrict__ status) {
@@ -533,15 +534,16 @@ __global__ void __launch_bounds__(kMoveRows) k_ev_move(EvSets sets,
   const int64_t first = (int64_t)blockIdx.x * kMoveRows;
   // survivors before this block
   uint32_t part = 0, before;
+  const bool keep = first + threadIdx.x < n && decisions[first + threadIdx.x] != 0;
   if (counts) {
+    wait_for_previous();  // the counts are there
     const unsigned g = groups ? blockIdx.x / kMoveGroup : 0u;
-    for (unsigned b = threadIdx.x; b < g; b += kMoveRows) part += groups[b];
+    for (unsigned b = threadIdx.x; b < g; b += kMoveRows) part += __ldcg(&groups[b]);
     for (unsigned b = g * kMoveGroup + threadIdx.x; b < blockIdx.x; b += kMoveRows)
-      part += counts[b];
+      part += __ldcg(&counts[b]);
   } else {
     part = survivors_part(decisions, 0, first, threadIdx.x, kMoveRows);
   }
-  const bool keep = first + threadIdx.x < n && decisions[first + threadIdx.x] != 0;
   block_scan<kWarps>(part, s_w, before);
   uint32_t m;
   const uint32_t o = block_scan<kWarps>(keep ? 1u : 0u, s_w, m);
@@ -672,9 +674,15 @@ cudaError_t launch_evict_compact(const DpTensorPtrs& p_in, const DpTensorPtrs& m
                     : k3 == 12 ? k_ev_move<float4, 3>
                     : k3 == 3  ? k_ev_move<float, 3>
                                : k_ev_move<float, kNoSh>;
-  move<<<grid, kMoveRows, 0, stream>>>(sets, decisions, n, capacity, counts, groups, source, n_out,
-                                       status);
-  return cudaGetLastError();
+  if (!counts) {
+    move<<<grid, kMoveRows, 0, stream>>>(sets, decisions, n, capacity, counts, groups, source,
+                                         n_out, status);
+    return cudaGetLastError();
+  }
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_dependent(move, grid, dim3(kMoveRows), stream, sets, decisions, n, capacity,
+                          (const uint32_t*)counts, (const uint32_t*)groups, source, n_out, status);
 }
 
 }  // namespace gsb

@@ -204,6 +204,17 @@ __device__ __forceinline__ uint32_t lanemask_lt() {
   return m;
 }
 
+// Dependent launches: a kernel started with launch_dependent (gs_internal.h)
+// may begin while the kernel before it on the stream still runs;
+// wait_for_previous returns when that one has finished and its writes are
+// there. let_next_begin, by every block of the kernel before, allows it early.
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void let_next_begin() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // One Adam update (lshu.cn sec. 3.3; Kingma and Ba with bias correction,
 // eps outside the square root); ibc1 = 1 / (1 - b1^t), ibc2 = 1 / (1 - b2^t).
 // The square root and the division use the SFU (a few ulp on the step, far

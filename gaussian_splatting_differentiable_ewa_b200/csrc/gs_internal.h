@@ -9,6 +9,24 @@
 
 namespace gsb {
 
+// Launch a kernel that may begin while the kernel before it on the stream
+// still runs, and that calls wait_for_previous before it touches anything that
+// one writes (everything earlier on the stream has finished by then).
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t stream,
+                             A... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Digits of a least-significant-digit radix sort: pass i orders by
 // (key >> shift[i]) & (2^bits[i] - 1).
 struct RadixPlan {

@@ -828,7 +828,9 @@ __device__ __forceinline__ float one_if(bool p, float x) {
 // an address: 9 cycles of the SM for a record's 36 bytes; the forward's (x, x)
 // pairs would take 18). On a 1M-Gaussian 1080p frame (4.4M entries of 8 x 8
 // blocks) the whole call takes 0.235 ms at 82 % of the issue slots, the
-// forward itself 0.494 ms. What was measured on the way: the block staging
+// forward itself 0.494 ms; on 1000 Gaussians at 128 x 128 three launches in
+// 0.017 ms (0.022 before the walk and the last kernel were allowed to begin
+// while the kernel before them ends). What was measured on the way: the block staging
 // batches of its tile's list as the forward does, 0.290 ms (barriers, and
 // lists padded per batch); bulk copies of the records, 0.277 ms (a bulk copy
 // is issued lane by lane); plain loads through registers, 0.243 ms; four
@@ -965,6 +967,7 @@ __global__ void __launch_bounds__(Shape<1>::kThreads) k_blend_weights(
   Own next = fetch_ids(0);
   issue(next, 0);
   Own after = fetch_ids(32);
+  wait_for_previous();  // the totals are cleared
   for (int buf = 0; head < tail; buf ^= 1) {
     const int n = min(32, tail - head);
     const Own mine = next;
@@ -1025,6 +1028,7 @@ __global__ void __launch_bounds__(Shape<1>::kThreads) k_blend_weights(
 __global__ void __launch_bounds__(256) k_weights_begin(unsigned long long* __restrict__ sums,
                                                        float* __restrict__ largest, int n,
                                                        float decay) {
+  let_next_begin();
   const int i = blockIdx.x * 256 + threadIdx.x;
   if (i >= n) return;
   sums[i] = 0ull;
@@ -1035,6 +1039,7 @@ __global__ void __launch_bounds__(256) k_weights_begin(unsigned long long* __res
 __global__ void __launch_bounds__(256) k_weights_end(const unsigned long long* __restrict__ sums,
                                                      float* __restrict__ weight_sum, int n,
                                                      float decay) {
+  wait_for_previous();
   const int i = blockIdx.x * 256 + threadIdx.x;
   if (i >= n) return;
   const double t = (double)sums[i] * (1.0 / 4294967296.0);
@@ -1089,11 +1094,15 @@ cudaError_t launch_blend_weights(const float* records, const uint32_t* ids, cons
                                              : k_blend_weights<true, false>)
                                : (weight_max ? k_blend_weights<false, true>
                                              : k_blend_weights<false, false>);
-  walk<<<(unsigned)tiles, Shape<1>::kThreads, 0, stream>>>(
-      records, ids, ranges, geo, n_contrib, warp_masks, pixel_weight, acc,
-      reinterpret_cast<uint32_t*>(weight_max), status);
-  k_weights_end<<<blocks, 256, 0, stream>>>(acc, weight_sum, n, decay);
-  return cudaGetLastError();
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess)
+    e = launch_dependent(walk, dim3((unsigned)tiles), dim3(Shape<1>::kThreads), stream, records,
+                         ids, ranges, geo, n_contrib, warp_masks, pixel_weight, acc,
+                         reinterpret_cast<uint32_t*>(weight_max), status);
+  if (e == cudaSuccess)
+    e = launch_dependent(k_weights_end, dim3(blocks), dim3(256), stream,
+                         (const unsigned long long*)acc, weight_sum, n, decay);
+  return e;
 }
 
 }  // namespace gsb

@@ -382,6 +382,47 @@ def test_captured_and_replayed_with_new_values():
         assert np.array_equal(dd.cpu().numpy(), O.evict_select(s.cpu().numpy(), None, keep))
 
 
+@pytest.mark.parametrize("n", [9000, 150_000, 700_001])
+def test_large_sets_captured_and_replayed(n):
+    """Selection by the grid and compaction behind its counts in one graph,
+    replayed with new scores (ties among them) and new rows."""
+    keep = (2 * n) // 3
+    score = torch.zeros(n, device="cuda")
+    d = torch.empty(n, dtype=torch.int8, device="cuda")
+    ws = _ws(api.gs_evict_workspace_size(n))
+    ins = _sets(n, 1, 3)
+    outs = [[torch.empty((keep,) + x.shape[1:], device="cuda") for x in a] for a in ins]
+    src = torch.empty(keep, dtype=torch.int32, device="cuda")
+    p, gi, go = api.params(*ins[0], 0), [api.grads(*a) for a in ins], [api.grads(*a) for a in outs]
+    side = torch.cuda.Stream()
+
+    def calls():
+        api.gs_evict_select(score, None, n, keep, d, ws, stream=side)
+        api.gs_evict_compact(p, gi[1], gi[2], d, go[0], go[1], go[2], keep, ws, source=src,
+                             stream=side)
+
+    torch.cuda.synchronize()
+    calls()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        calls()
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    for share in (0.0, 0.5, 1.0):
+        score.copy_(torch.rand(n, generator=gen, device="cuda"))
+        score[torch.rand(n, generator=gen, device="cuda") < share] = 0.0
+        for a in ins:
+            for x in a:
+                x.add_(1.0)
+        g.replay()
+        torch.cuda.synchronize()
+        rows = torch.sort(score, descending=True, stable=True).indices[:keep].sort().values
+        assert torch.equal(src.long(), rows)
+        for a, b in zip(ins, outs):
+            assert all(torch.equal(y, x[rows]) for x, y in zip(a, b))
+    assert api.gs_get_status(ws) == api.GS_OK
+
+
 def test_two_streams_with_their_own_workspaces():
     n = 200_000
     g = torch.Generator(device="cuda").manual_seed(1)
