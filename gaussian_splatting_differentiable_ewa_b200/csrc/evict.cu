@@ -11,10 +11,11 @@
 //  k_ev_select       small sets: one block, the keys in its registers, four
 //                    digits of 8 bits.
 //  k_ev_select_grid  larger sets: up to one block per SM, launched together;
-//                    the keys are read again for every digit (11 + 11 + 10
-//                    bits; from L2 up to some 25M Gaussians) and the counts
-//                    meet in global memory, behind a grid barrier with a time
-//                    limit.
+//                    three digits (11 + 11 + 10 bits) whose counts meet in
+//                    global memory, behind a grid barrier with a time limit.
+//                    Up to 1.2M Gaussians the keys stay in registers, above
+//                    that they are read again for every digit (from L2 up to
+//                    some 25M Gaussians).
 //
 // Compaction moves the survivors' rows in index order:
 //
@@ -207,8 +208,8 @@ __global__ void __launch_bounds__(kSelThreads) k_ev_select(const float* __restri
 
 // ------------------------------------------------------------ selection, large
 
-constexpr int kGridFlight = 2;                        // 16-byte reads in flight per thread
-constexpr int kWarpFlight = 2;                        // the same where warps go by themselves
+constexpr int kGridFlight = 2;                        // 16-byte reads in flight per lane
+constexpr int kWarpStep = 128 * kGridFlight;          // Gaussians a warp takes at a time
 constexpr int kCopies = 4;                            // counters per digit, by lane
 constexpr int kGridMin = kSelThreads;                 // Gaussians per block at least
 constexpr uint32_t kZeroKey = 0x80000000u;            // the key of a score of 0
@@ -225,32 +226,41 @@ struct Digit {
   __device__ static uint32_t of(uint32_t key) { return (key >> kShift) & (kBins - 1); }
 };
 
-// Keys of Gaussians i .. i + 3, by one 16-byte and one 4-byte read where VEC
-// says the pointers allow it. Scores that are neither negative nor NaN and
-// unprotected, as accumulated weights mostly are, take the short way: this
-// kernel is bound by its instructions per key.
+// Scores (bits) and protection of Gaussians i .. i + 3, by one 16-byte and one
+// 4-byte read where VEC says the pointers allow it.
+struct Raw4 {
+  uint32_t b[4], p;
+};
 template <bool VEC>
-__device__ __forceinline__ void ev_keys4(const float* __restrict__ score,
-                                         const uint8_t* __restrict__ protect, int64_t i,
-                                         uint32_t (&key)[4]) {
-  uint32_t b[4], p = 0;
+__device__ __forceinline__ Raw4 ev_read4(const float* __restrict__ score,
+                                         const uint8_t* __restrict__ protect, int64_t i) {
+  Raw4 r;
+  r.p = 0u;
   if (VEC) {
     const uint4 f = __ldg(reinterpret_cast<const uint4*>(score + i));
-    b[0] = f.x, b[1] = f.y, b[2] = f.z, b[3] = f.w;
-    if (protect) p = __ldg(reinterpret_cast<const uint32_t*>(protect + i));
+    r.b[0] = f.x, r.b[1] = f.y, r.b[2] = f.z, r.b[3] = f.w;
+    if (protect) r.p = __ldg(reinterpret_cast<const uint32_t*>(protect + i));
   } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      b[k] = __float_as_uint(__ldg(&score[i + k]));
-      if (protect && protect[i + k]) p |= 0xffu << (8 * k);
+    for (int k = 0; k < 4; ++k) r.b[k] = __float_as_uint(__ldg(&score[i + k]));
+    if (protect) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) r.p |= protect[i + k] ? 0xffu << (8 * k) : 0u;
     }
   }
-  if (max(max(b[0], b[1]), max(b[2], b[3])) <= 0x7f800000u && p == 0u) {
+  return r;
+}
+
+// Their keys. Scores that are neither negative nor NaN and unprotected, as
+// accumulated weights mostly are, take the short way.
+__device__ __forceinline__ void ev_keys4(const Raw4& r, uint32_t (&key)[4]) {
+  if (max(max(r.b[0], r.b[1]), max(r.b[2], r.b[3])) <= 0x7f800000u && r.p == 0u) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) key[k] = b[k] | 0x80000000u;
+    for (int k = 0; k < 4; ++k) key[k] = r.b[k] | 0x80000000u;
   } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) key[k] = ev_key(__uint_as_float(b[k]), (p >> (8 * k)) & 0xffu);
+    for (int k = 0; k < 4; ++k)
+      key[k] = ev_key(__uint_as_float(r.b[k]), (r.p >> (8 * k)) & 0xffu);
   }
 }
 
@@ -283,14 +293,50 @@ struct GridShared {
   bool ok;
 };
 
-// One digit of the wanted key over the block's Gaussians [first, end), then
-// over the grid. False: gave up at the barrier.
-template <int PASS, bool VEC>
-__device__ __forceinline__ bool grid_digit(GridShared& s, const float* __restrict__ score,
-                                           const uint8_t* __restrict__ protect, int64_t first,
-                                           int64_t end, EvictState* st, uint32_t& prefix,
-                                           uint32_t& want, uint32_t& equal, const WaitCfg& wc,
-                                           uint32_t* status) {
+// A warp's contiguous part [w0, w1) of the set, taken kWarpStep Gaussians at a
+// time, four consecutive ones per lane, as far as `whole`; then up to three
+// single ones. HELD: the part is one step, whose keys stay in registers.
+template <bool VEC, bool HELD>
+struct WarpPart {
+  const float* score;
+  const uint8_t* protect;
+  int64_t w0, w1, whole;
+  uint32_t key[kGridFlight][4];
+  uint32_t key1;  // of the lane's single one
+  bool single;
+
+  __device__ __forceinline__ int64_t at(int64_t i0, int f) const {
+    return i0 + 128 * f + 4 * (threadIdx.x & 31);
+  }
+  __device__ __forceinline__ void read(int64_t i0) {
+    Raw4 raw[kGridFlight];  // all reads before the first branch on one
+#pragma unroll
+    for (int f = 0; f < kGridFlight; ++f) {
+      raw[f] = Raw4{{0u, 0u, 0u, 0u}, 0u};
+      if (at(i0, f) < whole) raw[f] = ev_read4<VEC>(score, protect, at(i0, f));
+    }
+#pragma unroll
+    for (int f = 0; f < kGridFlight; ++f) ev_keys4(raw[f], key[f]);
+  }
+  __device__ __forceinline__ void begin(const float* s, const uint8_t* p, int64_t a, int64_t b) {
+    score = s, protect = p, w0 = a, w1 = b;
+    whole = w0 + ((w1 - w0) & ~(int64_t)3);
+    const int64_t i = whole + (threadIdx.x & 31);
+    single = i < w1;
+    key1 = single ? ev_key_at(score, protect, i) : 0u;
+    if (HELD) read(w0);
+  }
+  __device__ __forceinline__ void step(int64_t i0) {
+    if (!HELD) read(i0);
+  }
+};
+
+// One digit of the wanted key over the block's parts, then over the grid.
+// False: gave up at the barrier.
+template <int PASS, bool VEC, bool HELD>
+__device__ __forceinline__ bool grid_digit(GridShared& s, WarpPart<VEC, HELD>& part,
+                                           EvictState* st, uint32_t& prefix, uint32_t& want,
+                                           uint32_t& equal, const WaitCfg& wc, uint32_t* status) {
   using D = Digit<PASS>;
   static_assert(kCopies * sizeof(uint32_t) == sizeof(uint4), "one uint4 per digit");
   uint32_t* copies = reinterpret_cast<uint32_t*>(s.copies) + (threadIdx.x & (kCopies - 1));
@@ -306,25 +352,21 @@ __device__ __forceinline__ bool grid_digit(GridShared& s, const float* __restric
     else if (D::shares(key, prefix))
       atomicAdd(&copies[D::of(key) * kCopies], 1u);
   };
-  const int64_t whole = first + ((end - first) & ~(int64_t)3);
-  for (int64_t i = first + 4 * threadIdx.x; i < whole; i += 4 * kSelThreads * kGridFlight) {
-    uint32_t key[kGridFlight][4];
-#pragma unroll
-    for (int f = 0; f < kGridFlight; ++f)
-      if (i + 4 * kSelThreads * f < whole)
-        ev_keys4<VEC>(score, protect, i + 4 * kSelThreads * f, key[f]);
+  for (int64_t i0 = part.w0; i0 < part.whole; i0 += kWarpStep) {
+    part.step(i0);
 #pragma unroll
     for (int f = 0; f < kGridFlight; ++f) {
-      if (i + 4 * kSelThreads * f >= whole) continue;
+      if (part.at(i0, f) >= part.whole) continue;
+      const uint32_t(&key)[4] = part.key[f];
       // four keys at once that all differ from the wanted one above this digit
-      if (PASS > 0 && min(min(key[f][0] - prefix, key[f][1] - prefix),
-                          min(key[f][2] - prefix, key[f][3] - prefix)) >= D::kBins << D::kShift)
+      if (PASS > 0 && min(min(key[0] - prefix, key[1] - prefix),
+                          min(key[2] - prefix, key[3] - prefix)) >= D::kBins << D::kShift)
         continue;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) count(key[f][k]);
+      for (int k = 0; k < 4; ++k) count(key[k]);
     }
   }
-  if (whole + threadIdx.x < end) count(ev_key_at(score, protect, whole + threadIdx.x));
+  if (part.single) count(part.key1);
   zeros = __reduce_add_sync(0xffffffffu, zeros);
   if ((threadIdx.x & 31) == 0 && zeros && D::shares(kZeroKey, prefix))
     atomicAdd(&copies[D::of(kZeroKey) * kCopies], zeros);
@@ -358,60 +400,52 @@ __device__ __forceinline__ void put_decisions(int8_t* d, bool a, bool b, bool c,
   }
 }
 
-// Every block holds a contiguous share of the set (a multiple of 4).
-template <bool VEC>
+// Every block holds a contiguous share of the set, its warps contiguous parts
+// of that (`part` Gaussians, a multiple of 4), so that ties need no more than
+// the equal keys before each warp.
+template <bool VEC, bool HELD>
 __global__ void __launch_bounds__(kSelThreads) k_ev_select_grid(
     const float* __restrict__ score, const uint8_t* __restrict__ protect, int n, int n_keep,
-    int64_t share, EvictState* st, uint32_t* counts, int8_t* __restrict__ decisions, WaitCfg wc,
-    uint32_t* status) {
+    int64_t part_size, EvictState* st, uint32_t* counts, int8_t* __restrict__ decisions,
+    WaitCfg wc, uint32_t* status) {
   __shared__ GridShared s;
-  const int64_t first = blockIdx.x * share < n ? blockIdx.x * share : n;
-  const int64_t end = first + share < n ? first + share : n;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  WarpPart<VEC, HELD> part;
+  {
+    const int64_t a = ((int64_t)blockIdx.x * kSelWarps + warp) * part_size;
+    part.begin(score, protect, a < n ? a : n, a + part_size < n ? a + part_size : n);
+  }
   uint32_t t = 0, rank = (uint32_t)n_keep, equal = 0;
-  if (!grid_digit<0, VEC>(s, score, protect, first, end, st, t, rank, equal, wc, status) ||
-      !grid_digit<1, VEC>(s, score, protect, first, end, st, t, rank, equal, wc, status) ||
-      !grid_digit<2, VEC>(s, score, protect, first, end, st, t, rank, equal, wc, status))
+  if (!grid_digit<0>(s, part, st, t, rank, equal, wc, status) ||
+      !grid_digit<1>(s, part, st, t, rank, equal, wc, status) ||
+      !grid_digit<2>(s, part, st, t, rank, equal, wc, status))
     return;
 
-  // the decisions, a warp over a contiguous part of the block's share, so that
-  // ties need no more than the equal keys before each warp
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t part = ((end - first + 4 * kSelWarps - 1) / (4 * kSelWarps)) * 4;
-  const int64_t w0 = first + warp * part < end ? first + warp * part : end;
-  const int64_t w1 = w0 + part < end ? w0 + part : end;
-  const int64_t whole = w0 + ((w1 - w0) & ~(int64_t)3);  // then up to three single ones
-  const bool single = whole + lane < w1;
   if (equal == rank) {
-    for (int64_t i = w0 + 4 * lane; i < whole; i += 128 * kWarpFlight) {
-      uint32_t key[kWarpFlight][4];
+    for (int64_t i0 = part.w0; i0 < part.whole; i0 += kWarpStep) {
+      part.step(i0);
 #pragma unroll
-      for (int f = 0; f < kWarpFlight; ++f)
-        if (i + 128 * f < whole) ev_keys4<VEC>(score, protect, i + 128 * f, key[f]);
-#pragma unroll
-      for (int f = 0; f < kWarpFlight; ++f)
-        if (i + 128 * f < whole)
-          put_decisions<VEC>(decisions + i + 128 * f, key[f][0] >= t, key[f][1] >= t,
-                             key[f][2] >= t, key[f][3] >= t);
+      for (int f = 0; f < kGridFlight; ++f)
+        if (part.at(i0, f) < part.whole)
+          put_decisions<VEC>(decisions + part.at(i0, f), part.key[f][0] >= t,
+                             part.key[f][1] >= t, part.key[f][2] >= t, part.key[f][3] >= t);
     }
-    if (single) decisions[whole + lane] = ev_key_at(score, protect, whole + lane) >= t ? 1 : 0;
+    if (part.single) decisions[part.whole + lane] = part.key1 >= t ? 1 : 0;
     return;
   }
 
   // not all of the equal keys survive: those before this warp's
   uint32_t x = 0, total, before;
-  for (int64_t i = w0 + 4 * lane; i < whole; i += 128 * kWarpFlight) {
-    uint32_t key[kWarpFlight][4];
+  for (int64_t i0 = part.w0; i0 < part.whole; i0 += kWarpStep) {
+    part.step(i0);
 #pragma unroll
-    for (int f = 0; f < kWarpFlight; ++f)
-      if (i + 128 * f < whole) ev_keys4<VEC>(score, protect, i + 128 * f, key[f]);
+    for (int f = 0; f < kGridFlight; ++f)
+      if (part.at(i0, f) < part.whole) {
 #pragma unroll
-    for (int f = 0; f < kWarpFlight; ++f)
-      if (i + 128 * f < whole) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) x += key[f][k] == t;
+        for (int k = 0; k < 4; ++k) x += part.key[f][k] == t;
       }
   }
-  if (single) x += ev_key_at(score, protect, whole + lane) == t;
+  if (part.single) x += part.key1 == t;
   x = __reduce_add_sync(0xffffffffu, x);
   const uint32_t in_block =
       __shfl_sync(0xffffffffu, block_scan<kSelWarps>(lane == 0 ? x : 0u, s.w, total), 0);
@@ -421,19 +455,14 @@ __global__ void __launch_bounds__(kSelThreads) k_ev_select_grid(
   for (unsigned b = threadIdx.x; b < blockIdx.x; b += kSelThreads) y += __ldcg(&counts[b]);
   block_scan<kSelWarps>(y, s.w, before);
   before += in_block;
-  for (int64_t i0 = w0; i0 < whole; i0 += 128 * kWarpFlight) {
-    uint32_t key[kWarpFlight][4];
+  for (int64_t i0 = part.w0; i0 < part.whole; i0 += kWarpStep) {
+    part.step(i0);
 #pragma unroll
-    for (int f = 0; f < kWarpFlight; ++f) {
-      key[f][0] = key[f][1] = key[f][2] = key[f][3] = ~t;  // a lane past the end: not equal
-      if (i0 + 128 * f + 4 * lane < whole)
-        ev_keys4<VEC>(score, protect, i0 + 128 * f + 4 * lane, key[f]);
-    }
-#pragma unroll
-    for (int f = 0; f < kWarpFlight; ++f) {
+    for (int f = 0; f < kGridFlight; ++f) {
+      const bool in = part.at(i0, f) < part.whole;
       uint32_t eq = 0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) eq += key[f][k] == t;
+      for (int k = 0; k < 4; ++k) eq += in && part.key[f][k] == t;
       uint32_t incl = eq;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -445,17 +474,15 @@ __global__ void __launch_bounds__(kSelThreads) k_ev_select_grid(
       bool keep[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        keep[k] = key[f][k] > t || (key[f][k] == t && e < rank);
-        e += key[f][k] == t;
+        keep[k] = part.key[f][k] > t || (part.key[f][k] == t && e < rank);
+        e += part.key[f][k] == t;
       }
-      if (i0 + 128 * f + 4 * lane < whole)
-        put_decisions<VEC>(decisions + i0 + 128 * f + 4 * lane, keep[0], keep[1], keep[2],
-                           keep[3]);
+      if (in) put_decisions<VEC>(decisions + part.at(i0, f), keep[0], keep[1], keep[2], keep[3]);
     }
   }
-  const uint32_t key = single ? ev_key_at(score, protect, whole + lane) : ~t;
-  const uint32_t e = before + __popc(__ballot_sync(0xffffffffu, key == t) & lanemask_lt());
-  if (single) decisions[whole + lane] = key > t || (key == t && e < rank) ? 1 : 0;
+  const bool eq = part.single && part.key1 == t;
+  const uint32_t e = before + __popc(__ballot_sync(0xffffffffu, eq) & lanemask_lt());
+  if (part.single) decisions[part.whole + lane] = part.key1 > t || (eq && e < rank) ? 1 : 0;
 }
 
 // ------------------------------------------------------------ compaction
@@ -628,7 +655,8 @@ cudaError_t launch_evict_select(const float* score, const uint8_t* protect, int 
   // one block per SM, or one for every kGridMin Gaussians
   const int64_t want = ((int64_t)n + kGridMin - 1) / kGridMin;
   const int blocks = want < sms ? (int)want : sms;
-  const int64_t share = ((int64_t)n + 4 * (int64_t)blocks - 1) / (4 * (int64_t)blocks) * 4;
+  const int64_t warps = (int64_t)blocks * kSelWarps;
+  const int64_t part = ((int64_t)n + 4 * warps - 1) / (4 * warps) * 4;
   const bool vec = (reinterpret_cast<uintptr_t>(score) & 15) == 0 &&
                    (reinterpret_cast<uintptr_t>(protect) & 3) == 0 &&
                    (reinterpret_cast<uintptr_t>(decisions) & 3) == 0;
@@ -641,8 +669,11 @@ cudaError_t launch_evict_select(const float* score, const uint8_t* protect, int 
   cfg.numAttrs = 1;
   attr.id = cudaLaunchAttributeCooperative;  // all blocks at once, or an error
   attr.val.cooperative = 1;
-  return cudaLaunchKernelEx(&cfg, vec ? k_ev_select_grid<true> : k_ev_select_grid<false>, score,
-                            protect, n, n_keep, share, w.state, w.counts, decisions, wc, status);
+  const bool held = part <= kWarpStep;
+  const auto kernel = held ? (vec ? k_ev_select_grid<true, true> : k_ev_select_grid<false, true>)
+                           : (vec ? k_ev_select_grid<true, false> : k_ev_select_grid<false, false>);
+  return cudaLaunchKernelEx(&cfg, kernel, score, protect, n, n_keep, part, w.state, w.counts,
+                            decisions, wc, status);
 }
 
 cudaError_t launch_evict_compact(const DpTensorPtrs& p_in, const DpTensorPtrs& m_in,
