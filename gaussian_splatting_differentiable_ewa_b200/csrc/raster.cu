@@ -170,14 +170,24 @@ __device__ __forceinline__ uint32_t warp_block_mask(float u, float v, float hx, 
 // rasteriser's zq and the mean's float remainder, so no pixel the per-pixel
 // test takes is dropped; the axis-aligned box alone keeps ~40 % more (warp,
 // splat) pairs, whose ellipse misses the block.
-struct BlockEllipse {
-  float a, b, c, ia, ic, qm;
-  __device__ __forceinline__ BlockEllipse(float w1x, float w1y, float w2x, float w2y, float nlo)
-      : a(fmaf(w1x, w1x, w2x * w2x)), b(fmaf(w1x, w1y, w2x * w2y)), c(fmaf(w1y, w1y, w2y * w2y)),
-        ia(1.f / a), ic(1.f / c), qm(fmaf(-nlo, 1.002f, 0.01f)) {}
-  // the block [ex0, ex1] x [ey0, ey1] of pixel centres, relative to the mean
-  __device__ __forceinline__ bool reaches(float ex0, float ex1, float ey0, float ey1) const {
-    const bool hit = ex0 <= 0.f && ex1 >= 0.f && ey0 <= 0.f && ey1 >= 0.f;
+template <int NP>
+__device__ __forceinline__ uint32_t warp_block_mask_ellipse(const float* r, uint32_t box, int x0,
+                                                            int y0) {
+  constexpr int R = Shape<NP>::kBlockRows;
+  if (box == 0u) return 0u;
+  const float w1x = r[R_W1X], w1y = r[R_W1Y], w2x = r[R_W2X], w2y = r[R_W2Y];
+  const float a = fmaf(w1x, w1x, w2x * w2x), b = fmaf(w1x, w1y, w2x * w2y);
+  const float c = fmaf(w1y, w1y, w2y * w2y);
+  const float ia = 1.f / a, ic = 1.f / c;
+  const float qm = fmaf(-r[R_NLO], 1.002f, 0.01f);
+  const float u = r[R_U], v = r[R_V];
+  uint32_t mask = 0;
+#pragma unroll
+  for (int w = 0; w < Shape<NP>::kWarps; ++w) {
+    if (!((box >> w) & 1u)) continue;
+    const float ex0 = (float)(x0 + 8 * (w & 1)) + 0.5f - u, ex1 = ex0 + 7.f;
+    const float ey0 = (float)(y0 + R * (w >> 1)) + 0.5f - v, ey1 = ey0 + (float)(R - 1);
+    bool hit = ex0 <= 0.f && ex1 >= 0.f && ey0 <= 0.f && ey1 >= 0.f;
     float best = __int_as_float(0x7f800000);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -188,24 +198,8 @@ struct BlockEllipse {
       const float dx = fminf(fmaxf(-b * ey * ia, ex0), ex1);
       best = fminf(best, fmaf(c * ey, ey, fmaf(2.f * b * ey, dx, a * dx * dx)));
     }
-    return hit || best <= qm;
-  }
-};
-
-template <int NP>
-__device__ __forceinline__ uint32_t warp_block_mask_ellipse(const float* r, uint32_t box, int x0,
-                                                            int y0) {
-  constexpr int R = Shape<NP>::kBlockRows;
-  if (box == 0u) return 0u;
-  const BlockEllipse el(r[R_W1X], r[R_W1Y], r[R_W2X], r[R_W2Y], r[R_NLO]);
-  const float u = r[R_U], v = r[R_V];
-  uint32_t mask = 0;
-#pragma unroll
-  for (int w = 0; w < Shape<NP>::kWarps; ++w) {
-    if (!((box >> w) & 1u)) continue;
-    const float ex0 = (float)(x0 + 8 * (w & 1)) + 0.5f - u, ex1 = ex0 + 7.f;
-    const float ey0 = (float)(y0 + R * (w >> 1)) + 0.5f - v, ey1 = ey0 + (float)(R - 1);
-    mask |= el.reaches(ex0, ex1, ey0, ey1) ? 1u << w : 0u;
+    hit = hit || best <= qm;
+    mask |= hit ? 1u << w : 0u;
   }
   return mask;
 }
@@ -218,20 +212,6 @@ template <int NP>
 __device__ __noinline__ uint32_t record_block_mask(const float* r, int x0, int y0) {
   return warp_block_mask_ellipse<NP>(
       r, warp_block_mask<NP>(r[R_U], r[R_V], r[R_HX], r[R_HY], x0, y0), x0, y0);
-}
-
-// Both tests for one 8 x 8 pixel block at (xb, yb), on a record in global
-// memory.
-__device__ __noinline__ bool block_reached(const float* r, int xb, int yb) {
-  const float4* r4 = reinterpret_cast<const float4*>(r);
-  const float4 ra = __ldg(r4), rb = __ldg(r4 + 1), rd = __ldg(r4 + 3);
-  const float u = ra.x, v = ra.y, hx = rd.x, hy = rd.y;
-  const float xlo = (float)xb + 0.5f, ylo = (float)yb + 0.5f;
-  if (!(hx >= 0.f) || !(u + hx >= xlo && u - hx <= xlo + 7.f && v + hy >= ylo &&
-                        v - hy <= ylo + 7.f))
-    return false;
-  const BlockEllipse el(ra.z, ra.w, rb.y, rb.z, __ldg(r + R_NLO));
-  return el.reaches(xlo - u, xlo - u + 7.f, ylo - v, ylo - v + 7.f);
 }
 
 // The pixel-independent part of the evaluation at column pxc: dx = pxc - uh
@@ -771,281 +751,6 @@ __global__ void __launch_bounds__(Shape<NP>::kThreads) k_raster_bwd(
       mbar_wait_bounded(&s_bar[bf], (uint32_t)((pend[bf] >> 1) & 1), wc.limit_ns, status);
 }
 
-// Warp sums (or, with MAX, maxima) of kWeightGroup = 4 per-lane values by a
-// transposing butterfly: the first two exchanges halve the live values, three
-// more finish the one that is left: 6 shuffles instead of 20. Lane l returns
-// the result of value 2 ((l>>4)&1) + ((l>>3)&1).
-constexpr int kWeightGroup = 4;
-template <bool MAX>
-__device__ __forceinline__ float warp_reduce4(const float (&v)[kWeightGroup]) {
-  const int lane = threadIdx.x & 31;
-  const bool h16 = lane & 16, h8 = lane & 8;
-  auto op = [](float x, float y) { return MAX ? fmaxf(x, y) : x + y; };
-  float a[2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-    a[k] = op(h16 ? v[k + 2] : v[k],
-              __shfl_xor_sync(0xffffffffu, h16 ? v[k] : v[k + 2], 16));
-  float c = op(h8 ? a[1] : a[0], __shfl_xor_sync(0xffffffffu, h8 ? a[0] : a[1], 8));
-#pragma unroll
-  for (int o = 4; o > 0; o >>= 1) c = op(c, __shfl_xor_sync(0xffffffffu, c, o));
-  return c;
-}
-
-// 1 where p and x <= 0, else 0.
-__device__ __forceinline__ float one_if(bool p, float x) {
-  float r;
-  asm("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
-      "set.le.and.f32.f32 %0, %1, 0f00000000, q;\n\t}"
-      : "=f"(r)
-      : "f"(x), "r"((uint32_t)p));
-  return r;
-}
-
-// Accumulated blending weights (gs_blend_weights): per list entry the sum (and
-// with MAX the largest) over a tile's pixels of m w, w = alpha T the forward's
-// weight and m the pixel's weight in [0, 1]. The walk evaluates what the
-// forward evaluates (the same IEEE operations) without colours and without its
-// stop test: n_contrib already says how far each pixel composited. The weights
-// are linear in T, so T starts at m and the pixel weight costs nothing per
-// entry.
-//
-// Every warp works by itself on its 8 x 8 pixel block, two pixels per lane:
-// it scans the list for the entries that reach its block (the forward's masks,
-// or the block test), queues their positions, and takes them 32 at a time.
-// The first 48 bytes of the 32 records go to shared memory by 16-byte
-// asynchronous copies, three lanes to a record; the warp evaluates all of
-// them, four per transposing butterfly, which leaves each entry's result in
-// the lane that owns the entry; that lane adds it to the Gaussian's 64-bit
-// total in units of 2^-32 -- integers, so totals do not depend on the order in
-// which warps arrive. (A maximum of non-negative floats is a maximum of their
-// bits.) The next chunk's records, the one after's ids and the next masks are
-// in flight meanwhile; no warp waits for another, and only the last chunk of
-// a block is padded.
-//
-// What bounds it: instruction issue, and the shared-memory reads behind it (a
-// read returns 4 bytes to each of 32 lanes per cycle whether or not they share
-// an address: 9 cycles of the SM for a record's 36 bytes; the forward's (x, x)
-// pairs would take 18). On a 1M-Gaussian 1080p frame (4.4M entries of 8 x 8
-// blocks) the whole call takes 0.235 ms at 82 % of the issue slots, the
-// forward itself 0.494 ms; on 1000 Gaussians at 128 x 128 three launches in
-// 0.017 ms (0.022 before the walk and the last kernel were allowed to begin
-// while the kernel before them ends). What was measured on the way: the block staging
-// batches of its tile's list as the forward does, 0.290 ms (barriers, and
-// lists padded per batch); bulk copies of the records, 0.277 ms (a bulk copy
-// is issued lane by lane); plain loads through registers, 0.243 ms; four
-// pixels per lane, 0.251 ms; one warp per thread block, 0.233 ms.
-constexpr float kWeightUnit = 4294967296.f;  // 2^32
-constexpr int kWeightQueue = 256;            // positions a warp can hold
-constexpr int kWeightAhead = 96;             // positions it wants queued: three chunks
-constexpr int kWeightRow = 12;               // floats of a record the walk stages
-static_assert(R_NLO < kWeightRow, "the staged part holds the evaluation form");
-
-template <bool MASKS, bool MAX>
-__global__ void __launch_bounds__(Shape<1>::kThreads) k_blend_weights(
-    const float* __restrict__ records, const uint32_t* __restrict__ ids,
-    const int64_t* __restrict__ ranges, RasterGeom geo, const uint32_t* __restrict__ n_contrib,
-    const uint8_t* __restrict__ wmask_in, const float* __restrict__ pixel_weight,
-    unsigned long long* __restrict__ sums, uint32_t* __restrict__ largest,
-    uint32_t* __restrict__ status) {
-  constexpr int kWarps = Shape<1>::kWarps;
-  __shared__ __align__(16) float s_rec[kWarps][2][32][kWeightRow];
-  __shared__ __align__(16) uint32_t s_at[kWarps][32];
-  __shared__ uint32_t s_queue[kWarps][kWeightQueue];
-
-  const int tile = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const TilePix<1> tp = tile_pixel<1>(geo.g, tile);
-  const size_t hw = (size_t)geo.g.width * geo.g.height;
-  int64_t start, end;
-  tile_range(ranges, tile, geo.capacity, start, end, status);
-  const float* rec_view = records + (size_t)tp.view * geo.n * GS_RECORD_FLOATS;
-  const uint32_t lt = lanemask_lt();
-  // a pixel without weight takes no part (a NaN or negative weight counts as
-  // none)
-  float2 T;
-  uint32_t nc[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    nc[i] = 0;
-    float m = 1.f;
-    if (tp.in[i]) {
-      const size_t pix = (size_t)tp.view * hw + (size_t)(tp.py + 4 * i) * geo.g.width + tp.px;
-      nc[i] = n_contrib[pix];
-      if (pixel_weight) m = pixel_weight[pix];
-      if (!(m > 0.f)) {
-        nc[i] = 0;
-        m = 0.f;
-      }
-    }
-    (i ? T.y : T.x) = fminf(m, 1.f);
-  }
-  // the longest prefix among the warp's pixels; positions are 32-bit
-  const uint32_t wm = __reduce_max_sync(0xffffffffu, max(nc[0], nc[1]));
-  const int64_t used = end - start < (int64_t)wm ? end - start : (int64_t)wm;
-  const int limit = (int)(used < (int64_t)0x7fffff00 ? used : (int64_t)0x7fffff00);
-
-  uint32_t* queue = s_queue[warp];
-  int head = 0, tail = 0, scan = 0;  // positions consumed, queued, looked at
-  uint32_t mk[4];                    // MASKS: the masks of the next 128 positions
-  auto load_masks = [&] {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int p = scan + 32 * i + lane;
-      mk[i] = p < limit ? (uint32_t)wmask_in[start + p] : 0u;
-    }
-  };
-  auto push = [&](bool hit, int p) {
-    const uint32_t bal = __ballot_sync(0xffffffffu, hit);
-    if (hit) queue[(tail + __popc(bal & lt)) & (kWeightQueue - 1)] = (uint32_t)p;
-    tail += __popc(bal);
-  };
-  // queue positions until three chunks are there or the list has ended
-  auto fill = [&] {
-    while (tail - head < kWeightAhead && scan < limit) {
-      if (MASKS) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) push((mk[i] >> warp) & 1u, scan + 32 * i + lane);
-        scan += 128;
-        load_masks();
-      } else {
-        const int p = scan + lane;
-        bool hit = false;
-        if (p < limit) {
-          const uint32_t id = __ldg(&ids[start + p]);
-          // an entry that names no Gaussian goes through, to be reported
-          hit = id >= (uint32_t)geo.n ||
-                block_reached(rec_view + (size_t)id * GS_RECORD_FLOATS, tp.x0 + 8 * (warp & 1),
-                              tp.y0 + 8 * (warp >> 1));
-        }
-        push(hit, p);
-        scan += 32;
-      }
-    }
-    __syncwarp();
-  };
-
-  // lane l fetches (and adds up) entry `own` of every chunk: the one whose sum
-  // the butterflies leave in it
-  const int own = 4 * (lane & 7) + 2 * ((lane >> 4) & 1) + ((lane >> 3) & 1);
-  constexpr uint32_t kNone = 0xffffffffu;
-  struct Own {
-    uint32_t id, at;
-  };
-  auto fetch_ids = [&](int first) {  // of the chunk that starts at queue position `first`
-    Own o{kNone, 0u};
-    if (first + own < tail) {
-      o.at = queue[(first + own) & (kWeightQueue - 1)];
-      o.id = __ldg(&ids[start + o.at]);
-      if (o.id >= (uint32_t)geo.n) {  // never read outside the records
-        atomicOr(status, kStatusBounds);
-        o.id = kNone;
-      }
-    }
-    return o;
-  };
-  auto issue = [&](const Own& o, int buf) {
-    float(*rows)[kWeightRow] = s_rec[warp][buf];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 8 * i + (lane >> 2), q = lane & 3;
-      const uint32_t id =
-          __shfl_sync(0xffffffffu, o.id, (r >> 2) + 16 * ((r >> 1) & 1) + 8 * (r & 1));
-      if (id != kNone && q < 3)
-        copy_async16(&rows[r][4 * q], rec_view + (size_t)id * GS_RECORD_FLOATS + 4 * q);
-    }
-    copy_async_commit();
-    if (o.id == kNone) {  // no entry, or none with a Gaussian: zq = +inf at every pixel
-#pragma unroll
-      for (int i = 0; i < 9; ++i) rows[own][i] = i == R_NLO ? __int_as_float(0x7f800000) : 0.f;
-    }
-  };
-
-  const float pxc = (float)tp.px + 0.5f;
-  const float2 pyc = make_float2((float)tp.py + 0.5f, (float)tp.py + 4.5f);
-  if (MASKS) load_masks();
-  fill();
-  Own next = fetch_ids(0);
-  issue(next, 0);
-  Own after = fetch_ids(32);
-  wait_for_previous();  // the totals are cleared
-  for (int buf = 0; head < tail; buf ^= 1) {
-    const int n = min(32, tail - head);
-    const Own mine = next;
-    s_at[warp][own] = mine.at;
-    head += n;
-    // what comes next on its way
-    next = after;
-    issue(next, buf ^ 1);
-    fill();
-    after = fetch_ids(head + 32);
-    copy_async_wait_but_one();
-    __syncwarp();
-
-    float sum = 0.f, top = 0.f;
-    const int groups = (n + kWeightGroup - 1) / kWeightGroup;
-    for (int g = 0; g < groups; ++g) {
-      const float(*rec)[kWeightRow] = &s_rec[warp][buf][kWeightGroup * g];
-      const uint4 at4 = *reinterpret_cast<const uint4*>(&s_at[warp][kWeightGroup * g]);
-      const uint32_t at[kWeightGroup] = {at4.x, at4.y, at4.z, at4.w};
-      float v[kWeightGroup], t[kWeightGroup];  // of -w: -alpha saves sign changes in T (1 - alpha)
-#pragma unroll
-      for (int k = 0; k < kWeightGroup; ++k) {
-        const float4 ra = *reinterpret_cast<const float4*>(&rec[k][0]);  // u v w1x w1y
-        const float4 rb = *reinterpret_cast<const float4*>(&rec[k][4]);  // c1 w2x w2y c2
-        const float nlo = rec[k][R_NLO];
-        const float dx = __fsub_rn(pxc, ra.x);
-        const float a1 = __fmaf_rn(ra.z, dx, rb.x), a2 = __fmaf_rn(rb.y, dx, rb.w);
-        const float2 dy = make_float2(__fsub_rn(pyc.x, ra.y), __fsub_rn(pyc.y, ra.y));
-        const float2 p1 = __ffma2_rn(f2(ra.w), dy, f2(a1));
-        const float2 p2 = __ffma2_rn(f2(rb.z), dy, f2(a2));
-        const float2 zq = __ffma2_rn(p1, p1, __ffma2_rn(p2, p2, f2(nlo)));
-        const float2 raw = __fmul2_rn(make_float2(exp2f(-zq.x), exp2f(-zq.y)), f2(-kInv255));
-        const float2 on = make_float2(one_if(at[k] < nc[0], zq.x), one_if(at[k] < nc[1], zq.y));
-        const float2 na = __fmul2_rn(on, make_float2(fmaxf(-kAlphaMax, raw.x),
-                                                     fmaxf(-kAlphaMax, raw.y)));
-        const float2 nw = __fmul2_rn(na, T);
-        T = __ffma2_rn(na, T, T);
-        v[k] = nw.x + nw.y;
-        if (MAX) t[k] = fmaxf(-nw.x, -nw.y);
-      }
-      const float s = warp_reduce4<false>(v);
-      if ((lane & 7) == g) sum = -s;
-      if (MAX) {
-        const float m = warp_reduce4<true>(t);
-        if ((lane & 7) == g) top = m;
-      }
-    }
-    if (sum > 0.f) {  // an entry without a Gaussian sums to 0
-      atomicAdd(&sums[mine.id], __float2ull_rn(sum * kWeightUnit));
-      if (MAX) atomicMax(&largest[mine.id], __float_as_uint(top));
-    }
-    __syncwarp();  // the chunk's shared memory is free
-  }
-}
-
-// Before the walk: totals cleared, the kept maxima scaled (a decay of 0 reads
-// nothing). A kept maximum below zero or NaN counts as zero.
-__global__ void __launch_bounds__(256) k_weights_begin(unsigned long long* __restrict__ sums,
-                                                       float* __restrict__ largest, int n,
-                                                       float decay) {
-  let_next_begin();
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= n) return;
-  sums[i] = 0ull;
-  if (largest) largest[i] = decay > 0.f ? fmaxf(decay * largest[i], 0.f) : 0.f;
-}
-
-// After the walk: sum <- decay sum + total, in double, rounded once.
-__global__ void __launch_bounds__(256) k_weights_end(const unsigned long long* __restrict__ sums,
-                                                     float* __restrict__ weight_sum, int n,
-                                                     float decay) {
-  wait_for_previous();
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= n) return;
-  const double t = (double)sums[i] * (1.0 / 4294967296.0);
-  weight_sum[i] = (float)(decay > 0.f ? fma((double)decay, (double)weight_sum[i], t) : t);
-}
-
 }  // namespace
 
 cudaError_t launch_raster_fwd(const float* records, const uint32_t* ids, const int64_t* ranges,
@@ -1077,32 +782,6 @@ cudaError_t launch_raster_bwd(const float* records, const uint32_t* ids, const i
       grad2d,
       status, wc);
   return cudaGetLastError();
-}
-
-cudaError_t launch_blend_weights(const float* records, const uint32_t* ids, const int64_t* ranges,
-                                 int64_t capacity, const Grid& g, int n_views, int n,
-                                 const uint32_t* n_contrib, const uint8_t* warp_masks,
-                                 const float* pixel_weight, float decay, float* weight_sum,
-                                 float* weight_max, uint64_t* sums, uint32_t* status,
-                                 cudaStream_t stream) {
-  const int64_t tiles = (int64_t)g.tiles_per_view * n_views;
-  const unsigned blocks = (unsigned)((n + 255) / 256);
-  unsigned long long* acc = reinterpret_cast<unsigned long long*>(sums);
-  k_weights_begin<<<blocks, 256, 0, stream>>>(acc, weight_max, n, decay);
-  RasterGeom geo{g, n, capacity};
-  const auto walk = warp_masks ? (weight_max ? k_blend_weights<true, true>
-                                             : k_blend_weights<true, false>)
-                               : (weight_max ? k_blend_weights<false, true>
-                                             : k_blend_weights<false, false>);
-  cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess)
-    e = launch_dependent(walk, dim3((unsigned)tiles), dim3(Shape<1>::kThreads), stream, records,
-                         ids, ranges, geo, n_contrib, warp_masks, pixel_weight, acc,
-                         reinterpret_cast<uint32_t*>(weight_max), status);
-  if (e == cudaSuccess)
-    e = launch_dependent(k_weights_end, dim3(blocks), dim3(256), stream,
-                         (const unsigned long long*)acc, weight_sum, n, decay);
-  return e;
 }
 
 }  // namespace gsb
