@@ -351,7 +351,7 @@ cudaError_t launch_blend_weights(const float* records, const uint32_t* ids, cons
                                  float* weight_max, uint64_t* sums, uint32_t* status,
                                  cudaStream_t stream) {
   const int64_t tiles = (int64_t)g.tiles_per_view * n_views;
-  const unsigned blocks = (unsigned)((n + 255) / 256);
+  const unsigned blocks = (unsigned)(((int64_t)n + 255) / 256);
   unsigned long long* acc = reinterpret_cast<unsigned long long*>(sums);
   k_weights_begin<<<blocks, 256, 0, stream>>>(acc, weight_max, n, decay);
   WeightGeom geo{g, n, capacity};

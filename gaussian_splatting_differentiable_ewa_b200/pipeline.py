@@ -223,6 +223,7 @@ class Splatter:
         api.gs_rasterize_fwd(self.c_proj, self.c_bins, self.cams, self.V, self.n, self.bg,
                              self.image if image is None else image, self.final_T,
                              self.n_contrib, self.ws, self.stream, warp_masks=self.warp_masks)
+        self._frame_gen = self._gen  # the buffers that hold this frame
 
     def rasterize_bwd(self, dL_dimage: torch.Tensor, with_params: bool = True):
         api.gs_rasterize_bwd(self.c_params, self.c_proj, self.c_bins, self.cams, self.V, self.bg,
@@ -643,11 +644,14 @@ class Splatter:
     # ------------------------------------------------------------ eviction
     def accumulate_weights(self, pixel_weight: Optional[torch.Tensor] = None,
                            decay: float = 1.0, largest: bool = False) -> torch.Tensor:
-        """Add the blending weights of the frame just rendered (forward or
-        rasterize_fwd) to ``self.weight_sum``, scaled by `decay` first, and with
-        `largest` their maxima to ``self.weight_max`` (gs_blend_weights).
-        pixel_weight: float32 [V, H, W] in [0, 1], a mask or an error map.
-        Both start from zero and restart with every new Gaussian set."""
+        """Add the blending weights of the last rendered frame (forward,
+        rasterize_fwd, a training step) to ``self.weight_sum``, scaled by
+        `decay` first, and with `largest` their maxima to ``self.weight_max``
+        (gs_blend_weights). pixel_weight: float32 [V, H, W] in [0, 1], a mask
+        or an error map. Both start from zero and restart with every new
+        Gaussian set."""
+        if getattr(self, "_frame_gen", None) != self._gen:
+            raise ValueError("no frame in the current buffers: render one first")
         if pixel_weight is not None and (tuple(pixel_weight.shape) != (self.V, self.H, self.W)
                                          or pixel_weight.dtype != torch.float32
                                          or pixel_weight.device != self.ws.device

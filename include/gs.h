@@ -494,7 +494,9 @@ gs_status gs_densify_and_prune(const gs_params* in, const gs_grads* m_in, const 
  * the weights and the background's T_final sum to one. Summed over pixels and
  * views, a Gaussian's weights say how much the renders draw on it; holding
  * the set to a budget evicts those that they draw on least. The pages only
- * prune by opacity and scale; these calls hold a count. */
+ * prune by opacity and scale; these calls hold a count. A call keeps its
+ * scratch in its workspace until its work is done: calls (or graphs) whose
+ * work may overlap need workspaces of their own. */
 
 /* Bytes of workspace gs_blend_weights needs for n Gaussians (256-byte
  * aligned; the first 256 bytes hold the status word, zeroed once). */

@@ -171,6 +171,9 @@ def test_splatter_refuses_on_the_host():
     for bad in (torch.zeros(50), torch.zeros(49, dtype=torch.uint8)):
         with pytest.raises(ValueError, match="protect"):
             sp.evict(10, score=score, protect=bad)
+    with pytest.raises(ValueError, match="render"):
+        sp.accumulate_weights()
+    sp._frame_gen = sp._gen            # as after a render
     for bad in (torch.zeros(1, 128, 127), torch.zeros(1, 128, 128, dtype=torch.float64),
                 torch.zeros(1, 128, 256)[:, :, ::2]):
         with pytest.raises(ValueError, match="pixel_weight"):

@@ -333,6 +333,8 @@ def test_compaction_capacity_any_nonzero_and_empty():
     for a, b in zip(ins, outs):
         for x, y in zip(a, b):
             assert torch.equal(y[:1500], x[10:1510]) and torch.all(y[1500:] == 5.0)
+    _, src, n_out, st = _compact(ins, 1, d, 0)                     # no room at all
+    assert st == api.GS_ERR_CAPACITY and n_out == 3990 and torch.all(src == -7)
     outs, _, n_out, st = _compact(ins, 1, d, 4100, source=False)   # room to spare
     assert st == api.GS_OK and n_out == 3990
     assert torch.equal(outs[2][4][:3990], ins[2][4][10:4000])
@@ -441,6 +443,45 @@ def test_two_streams_with_their_own_workspaces():
             api.gs_evict_select(scores[k], None, n, n // 2, d[k], ws[k], stream=streams[k])
     torch.cuda.synchronize()
     assert torch.equal(d[0], want[0]) and torch.equal(d[1], want[1])
+
+
+def test_large_selections_side_by_side():
+    """Grids that wait for their own blocks, on streams of different priority,
+    beside one another and beside other work: all finish, none gives up."""
+    n = 3_000_000
+    g = torch.Generator(device="cuda").manual_seed(2)
+    scores = [torch.rand(n, generator=g, device="cuda") for _ in range(3)]
+    want = []
+    for s in scores:
+        w = torch.zeros(n, dtype=torch.int8, device="cuda")
+        w[torch.sort(s, descending=True, stable=True).indices[:n // 3]] = 1
+        want.append(w)
+    d = [torch.empty(n, dtype=torch.int8, device="cuda") for _ in range(3)]
+    ws = [_ws(api.gs_evict_workspace_size(n)) for _ in range(3)]
+    streams = [torch.cuda.Stream(priority=p) for p in (0, -1, 0)]
+    busy = torch.cuda.Stream(priority=-1)
+    filler = torch.zeros(1 << 24, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for k in range(3):
+            api.gs_evict_select(scores[k], None, n, n // 3, d[k], ws[k], stream=streams[k])
+        with torch.cuda.stream(busy):
+            filler.add_(1.0)
+    torch.cuda.synchronize()
+    for k in range(3):
+        assert api.gs_get_status(ws[k], streams[k]) == api.GS_OK
+        assert torch.equal(d[k], want[k])
+
+
+def test_splatter_wants_a_frame_of_the_current_set():
+    sp = _frame("fwd_1k_128")
+    sp.accumulate_weights()
+    sp.evict(500)
+    with pytest.raises(ValueError, match="render"):
+        sp.accumulate_weights()
+    sp.ensure_capacity()
+    sp.rasterize_fwd()
+    assert float(sp.accumulate_weights().sum()) > 0 and sp.weights_status() == api.GS_OK
 
 
 @pytest.mark.parametrize("bits", [None, 8, 16])
