@@ -97,6 +97,8 @@ __device__ __forceinline__ void find_digit(const uint32_t (&c)[PER], uint32_t wa
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelKeys = 8;  // keys per thread, in registers
+// Up to here one block: at 8,192 Gaussians 9.4 us against 12.6 for the grid,
+// whose barriers cost more than the block's longer passes (1,000: 6 us).
 constexpr int kSelMax = kSelThreads * kSelKeys;
 
 // The warps hold consecutive spans of 32 per_thread Gaussians; lane l of a
@@ -211,7 +213,9 @@ __global__ void __launch_bounds__(kSelThreads) k_ev_select(const float* __restri
 constexpr int kGridFlight = 2;                        // 16-byte reads in flight per lane
 constexpr int kWarpStep = 128 * kGridFlight;          // Gaussians a warp takes at a time
 constexpr int kCopies = 4;                            // counters per digit, by lane
-constexpr int kGridMin = kSelThreads;                 // Gaussians per block at least
+constexpr int kGridMin = 2 * kSelThreads;             // Gaussians per block at least: fewer
+                                                      // blocks meet faster (16,000: 11.2 us
+                                                      // against 12.5 with 1,024)
 constexpr uint32_t kZeroKey = 0x80000000u;            // the key of a score of 0
 
 // Digit PASS of a key, the most significant first, and the bits above it.
@@ -293,9 +297,16 @@ struct GridShared {
   bool ok;
 };
 
+// The grid's time is latency: about 3 us for each of the three or (with ties at
+// the threshold) four phases between barriers -- counting, the counters'
+// additions in L2, the barrier, reading the counters back -- and above a few
+// million Gaussians the keys' own instructions and reads: 60,000 in 12.5 us,
+// 1.2M in 14, 10M in 45 (their 50 MB alone would take 8).
+//
 // A warp's contiguous part [w0, w1) of the set, taken kWarpStep Gaussians at a
 // time, four consecutive ones per lane, as far as `whole`; then up to three
-// single ones. HELD: the part is one step, whose keys stay in registers.
+// single ones. HELD: the part is one step, whose keys stay in registers (1.2M
+// Gaussians: 13.7 us against 15.3 when they are read again).
 template <bool VEC, bool HELD>
 struct WarpPart {
   const float* score;
@@ -489,7 +500,10 @@ __global__ void __launch_bounds__(kSelThreads) k_ev_select_grid(
 
 constexpr int kMoveRows = 256;     // Gaussians (and threads) per block
 constexpr int kMoveGroup = 1024;   // blocks per group total
-constexpr int kMoveDirect = 32768; // up to here blocks read the decisions before theirs
+// Up to here every block reads the decisions before its own instead of counts
+// from a kernel before it: at 16,000 Gaussians 4.8 us against 5.0, at 24,000
+// 5.8 against 5.2 (the reads grow with the square of the set).
+constexpr int kMoveDirect = 16384;
 
 // Nonzero bytes of a word.
 __device__ __forceinline__ uint32_t nonzero_bytes(uint32_t x) {
@@ -544,7 +558,13 @@ struct EvSets {
   EvSet s[3];
 };
 
-// SH rows of PER elements of type E (kNoSh: none).
+// Bound by HBM: 4M Gaussians of SH degree 3 with moments, 85 % kept, move 5.1 GB
+// in 0.77 ms, 6.7 TB/s (the plain copy's rate). One array set per block keeps
+// small sets on enough SMs (100,000: 20 us; all sets in blocks of 1,024
+// Gaussians took 95); 256 rows let every thread fetch one row's 52 bytes of
+// small fields at once, then six elements of the SH rows. Rows of PER elements
+// of type E there (kNoSh: none); 27 floats go one by one (0.4 of 778,000: 23
+// us, 5.3 TB/s with the sectors read in part).
 constexpr int kNoSh = -1;
 template <typename E, int PER>
 __global__ void __launch_bounds__(kMoveRows) k_ev_move(EvSets sets,

@@ -545,7 +545,7 @@ size_t gs_evict_workspace_size(int64_t n);
  * and 0 for the others. With more protected Gaussians than n_keep the lowest
  * indices among them survive (their scores do not count). Exact: the
  * threshold is an order statistic of the scores' bits. One launch; above
- * 131,072 Gaussians its blocks, one per SM, run together and wait for one
+ * 8,192 Gaussians its blocks, up to one per SM, run together and wait for one
  * another: GS_STATUS_BIT_TIMEOUT when that took too long (the decisions are
  * then not all written). */
 gs_status gs_evict_select(const float* score, const uint8_t* protect, int64_t n, int64_t n_keep,
@@ -688,7 +688,7 @@ gs_status gs_densify_sh_quant(const gs_sh_quant* in, const uint16_t* m_in, const
  *     single-sweep radix passes (the depth keys of GS_SORT_PRESORT, the pair
  *     keys of GS_SORT_FULL64) publishes neither its digit counts nor its
  *     prefix in any pass, so the waits of the partitions after it run out;
- *     in gs_evict_select above 131,072 Gaussians, block `index` never comes
+ *     in gs_evict_select above 8,192 Gaussians, block `index` never comes
  *     to the barrier of the launch;
  *   GS_STALL_NONE  back to normal.
  * wait_limit_s (> 0) replaces the default limit of 2 s for every wait while
