@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import contextlib
 import math
+import weakref
 from typing import Optional
 
 import numpy as np
@@ -29,6 +30,18 @@ DEFAULT_LR = dict(means=1.6e-4, sh=2.5e-3, opacity_logit=5e-2, log_scales=5e-3, 
 # this many floats, so that they split into 16-byte aligned equal slices for
 # any power-of-two number of ranks up to 256.
 FLAT_PAD = 1024
+
+
+class _CallGraph(torch.cuda.CUDAGraph):
+    """A CUDA graph of one call whose replay also takes the note that the call
+    takes on the host (`note`, a weak reference to a bound method, or None)."""
+    note = None
+
+    def replay(self) -> None:
+        super().replay()
+        note = self.note and self.note()
+        if note is not None:
+            note()
 
 
 class Splatter:
@@ -211,19 +224,29 @@ class Splatter:
         return need
 
     # ------------------------------------------------------------ the calls
+    # Records, lists and the rasteriser's outputs belong to one frame from a
+    # render until a projection or a sort writes over its records or lists.
+    def _frame_gone(self) -> None:
+        self._frame_gen = None
+
+    def _frame_rendered(self) -> None:
+        self._frame_gen = self._gen  # the buffers that hold this frame
+
     def project(self):
         api.gs_project(self.c_params, self.cams, self.V, self.c_proj, self.ws, self.stream)
+        self._frame_gone()
 
     def bin_sort(self):
         api.gs_bin_sort(self.c_proj, self.cams, self.V, self.n, self.sort_mode, self.c_bins,
                         self.ws, self.stream)
+        self._frame_gone()
 
     def rasterize_fwd(self, image: Optional[torch.Tensor] = None):
         """Render into ``self.image`` (or `image`, a tensor of its shape)."""
         api.gs_rasterize_fwd(self.c_proj, self.c_bins, self.cams, self.V, self.n, self.bg,
                              self.image if image is None else image, self.final_T,
                              self.n_contrib, self.ws, self.stream, warp_masks=self.warp_masks)
-        self._frame_gen = self._gen  # the buffers that hold this frame
+        self._frame_rendered()
 
     def rasterize_bwd(self, dL_dimage: torch.Tensor, with_params: bool = True):
         api.gs_rasterize_bwd(self.c_params, self.c_proj, self.c_bins, self.cams, self.V, self.bg,
@@ -340,9 +363,11 @@ class Splatter:
             (self.weight_sum,) if with_weights else (), (self.m_flat, self.v_flat),
             None if sh is None else (sh["lo"], sh["hi"]), None if sh is None else sh["group"])
 
-    def _graph_of(self, fn) -> "torch.cuda.CUDAGraph":
+    def _graph_of(self, fn, note=None) -> "torch.cuda.CUDAGraph":
         """A CUDA graph of one fixed-shape call: run once outside capture (on
-        a capture stream ordered after the current one), then captured."""
+        a capture stream ordered after the current one), then captured. `note`:
+        what the call notes on the host (a bound method), repeated by every
+        replay."""
         saved = self.stream
         cap = torch.cuda.Stream(device=self.device)
         cap.wait_stream(torch.cuda.current_stream(self.device))
@@ -353,10 +378,11 @@ class Splatter:
                 self.stream = cap
                 fn()
             cap.synchronize()
-            g = torch.cuda.CUDAGraph()
+            g = _CallGraph()
             with torch.cuda.graph(g, stream=cap):
                 self.stream = cap
                 fn()
+            g.note = None if note is None else weakref.WeakMethod(note)
         finally:
             self.stream = saved
         torch.cuda.current_stream(self.device).wait_stream(cap)
@@ -377,11 +403,13 @@ class Splatter:
         (ensure_capacity growing the pairs, densify_and_prune)."""
         calls = {"project": self.project, "bin_sort": self.bin_sort,
                  "rasterize_fwd": self.rasterize_fwd}
+        notes = {"project": self._frame_gone, "bin_sort": self._frame_gone,
+                 "rasterize_fwd": self._frame_rendered}
         if dL_dimage is not None:
             calls["rasterize_bwd"] = lambda: self.rasterize_bwd(dL_dimage, with_params=False)
             calls["project_bwd"] = self.project_bwd
             calls["densify_stats"] = self.densify_stats
-        return {name: self._graph_of(fn) for name, fn in calls.items()}
+        return {name: self._graph_of(fn, notes.get(name)) for name, fn in calls.items()}
 
     def forward(self):
         self.project()
@@ -464,9 +492,9 @@ class Splatter:
         # gradient buffer), kept until a buffer is reallocated
         hg = getattr(self, "_host_graphs", None)
         if hg is None or hg[0] != self._gen:
-            gr = {"project": self._graph_of(self.project),
-                  "bin_sort": self._graph_of(self.bin_sort),
-                  "rasterize_fwd": self._graph_of(self.rasterize_fwd)}
+            gr = {"project": self._graph_of(self.project, self._frame_gone),
+                  "bin_sort": self._graph_of(self.bin_sort, self._frame_gone),
+                  "rasterize_fwd": self._graph_of(self.rasterize_fwd, self._frame_rendered)}
             for b in range(2):
                 gr["bwd%d" % b] = self._graph_of(
                     lambda b=b: self.rasterize_bwd(self._dL_dev[b], with_params=False))
@@ -542,10 +570,11 @@ class Splatter:
         rg = getattr(self, "_render_graphs", None)
         if rg is None or rg[0] != self._gen:
             imgs = [self.image, torch.empty_like(self.image)]
-            gr = {"project": self._graph_of(self.project),
-                  "bin_sort": self._graph_of(self.bin_sort)}
+            gr = {"project": self._graph_of(self.project, self._frame_gone),
+                  "bin_sort": self._graph_of(self.bin_sort, self._frame_gone)}
             for b in range(2):
-                gr["fwd%d" % b] = self._graph_of(lambda b=b: self.rasterize_fwd(imgs[b]))
+                gr["fwd%d" % b] = self._graph_of(lambda b=b: self.rasterize_fwd(imgs[b]),
+                                                 self._frame_rendered)
             self._render_graphs = rg = (self._gen, gr, imgs)
         gr, imgs = rg[1], rg[2]
         rendered = torch.cuda.Event()
@@ -649,9 +678,12 @@ class Splatter:
         `decay` first, and with `largest` their maxima to ``self.weight_max``
         (gs_blend_weights). pixel_weight: float32 [V, H, W] in [0, 1], a mask
         or an error map. Both start from zero and restart with every new
-        Gaussian set."""
+        Gaussian set. Once project, bin_sort or ensure_capacity has run after
+        the render, or the buffers were reallocated, the frame is gone and a
+        ValueError asks for the next one; replays of capture_calls' graphs
+        count as their calls, graphs that the caller captured are not seen."""
         if getattr(self, "_frame_gen", None) != self._gen:
-            raise ValueError("no frame in the current buffers: render one first")
+            raise ValueError("the buffers hold no whole frame: render one first")
         if pixel_weight is not None and (tuple(pixel_weight.shape) != (self.V, self.H, self.W)
                                          or pixel_weight.dtype != torch.float32
                                          or pixel_weight.device != self.ws.device

@@ -1,0 +1,82 @@
+"""Accumulated weights and eviction through the Splatter on the GPU: frames that
+graphs render or overwrite."""
+
+import pytest
+import torch
+
+from gaussian_splatting_differentiable_ewa_b200 import api
+from gaussian_splatting_differentiable_ewa_b200 import scenes as S
+from gaussian_splatting_differentiable_ewa_b200.pipeline import Splatter
+
+pytestmark = pytest.mark.gpu
+
+
+def _splatter(n=2000, stream=None, **kw):
+    sp = Splatter(S.make_scene("fwd_100k_800", n=n, width=160, height=120), stream=stream, **kw)
+    torch.cuda.synchronize()
+    sp.ensure_capacity()
+    sp.rasterize_fwd()
+    torch.cuda.synchronize()
+    return sp
+
+
+def test_weights_of_moved_parameters_want_their_own_render():
+    """Parameters move, ensure_capacity finds room and writes their lists: the
+    old frame's weights are gone, the new frame's come with its render."""
+    sp = _splatter()
+    first = sp.accumulate_weights(decay=0.0).clone()
+    gen = sp._gen
+    sp.means[:, 0] += 0.05
+    sp.ensure_capacity()
+    assert sp._gen == gen                      # nothing was reallocated
+    with pytest.raises(ValueError, match="render"):
+        sp.accumulate_weights(decay=0.0)
+    sp.rasterize_fwd()
+    second = sp.accumulate_weights(decay=0.0).clone()
+    assert not torch.equal(first, second)
+    # the weights and the transmittance of the new frame sum to one per pixel:
+    # each of n_contrib entries is off by at most four roundings (2^-24)
+    tol = float((sp.n_contrib.double() + 4).sum()) * 2.0 ** -22
+    assert abs(float(second.double().sum() + sp.final_T.double().sum()) - sp.W * sp.H) <= tol
+
+
+def test_replayed_calls_count_as_the_calls():
+    sp = _splatter()
+    want = sp.accumulate_weights(decay=0.0).clone()
+    graphs = sp.capture_calls(torch.full_like(sp.image, 1e-3))
+    torch.cuda.synchronize()
+    assert torch.equal(sp.accumulate_weights(decay=0.0), want)
+    for name in ("project", "bin_sort"):
+        graphs[name].replay()
+        with pytest.raises(ValueError, match="render"):
+            sp.accumulate_weights(decay=0.0)
+        graphs["bin_sort"].replay()
+        graphs["rasterize_fwd"].replay()
+        assert torch.equal(sp.accumulate_weights(decay=0.0), want)
+        for after in ("rasterize_bwd", "project_bwd", "densify_stats"):
+            graphs[after].replay()
+            assert torch.equal(sp.accumulate_weights(decay=0.0), want)
+
+
+def test_host_fed_paths_leave_a_frame():
+    """train_from_host and render_to_host replay graphs of their own: their
+    last frame can be weighed, after a call that had spoilt the one before."""
+    stream = torch.cuda.Stream()
+    sp = _splatter(stream=stream)
+    shape = tuple(sp.image.shape)
+    images = [torch.empty(shape).pin_memory() for _ in range(3)]
+    grads = [torch.full(shape, 1e-4).pin_memory() for _ in range(3)]
+    with torch.cuda.stream(stream):
+        for run in (lambda: sp.render_to_host(images), lambda: sp.train_from_host(grads, images)):
+            for _ in range(2):                 # the second time nothing is captured
+                run()
+                got = sp.accumulate_weights(decay=0.0).clone()
+                torch.cuda.synchronize()
+                total = float(got.double().sum() + sp.final_T.double().sum())
+                tol = float((sp.n_contrib.double() + 4).sum()) * 2.0 ** -22
+                assert abs(total - sp.W * sp.H) <= tol
+                sp.project()
+                with pytest.raises(ValueError, match="render"):
+                    sp.accumulate_weights(decay=0.0)
+    torch.cuda.synchronize()
+    assert sp.status() == api.GS_OK and sp.weights_status() == api.GS_OK
