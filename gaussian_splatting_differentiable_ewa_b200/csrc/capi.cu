@@ -636,7 +636,7 @@ gs_status gs_densify_and_prune(const gs_params* in, const gs_grads* m_in, const 
 
 size_t gs_blend_weights_workspace_size(int64_t n) {
   if (n < 0 || n >= (1ll << 31)) return 0;
-  return align_up(kControlBytes + (size_t)n * sizeof(uint64_t));  // fixed-point totals
+  return align_up(kControlBytes + (size_t)n * (sizeof(uint64_t) + sizeof(uint32_t)));  // fixed-point totals
 }
 
 gs_status gs_blend_weights(const gs_projected* proj, const gs_binned* bins, const gs_camera* cams,
@@ -650,7 +650,7 @@ gs_status gs_blend_weights(const gs_projected* proj, const gs_binned* bins, cons
     return GS_ERR_INVALID_ARG;
   if (n >= (1ll << 31)) return GS_ERR_OVERFLOW;
   const Grid g = grid_of(cams[0]);
-  // a total counts every pixel at most once, in units of 2^-32 of 64 bits
+  // a total counts every pixel at most once, in units of 2^-32 or finer ones
   if ((int64_t)g.width * g.height > (1ll << 31) / n_views) return GS_ERR_OVERFLOW;
   if (ws_bytes < gs_blend_weights_workspace_size(n)) return GS_ERR_INVALID_ARG;
   if (n == 0) return GS_OK;

@@ -151,7 +151,7 @@ cudaError_t launch_raster_bwd(const float* records, const uint32_t* ids, const i
                               const uint32_t* n_contrib, const uint8_t* warp_masks,
                               float* grad2d, uint32_t* status, const WaitCfg& wc,
                               cudaStream_t stream);
-// Accumulated blending weights: `sums` is n 64-bit words of scratch.
+// Accumulated blending weights: `sums` is 12 n bytes of scratch.
 cudaError_t launch_blend_weights(const float* records, const uint32_t* ids, const int64_t* ranges,
                                  int64_t capacity, const Grid& g, int n_views, int n,
                                  const uint32_t* n_contrib, const uint8_t* warp_masks,

@@ -10,6 +10,8 @@
 
 #include <cuda_runtime.h>
 
+#include <cmath>
+
 #include "gs_internal.h"
 
 namespace gsb {
@@ -22,6 +24,7 @@ struct WeightGeom {
   Grid g;
   int n;
   int64_t capacity;  // length of ids
+  float whole;       // 2^k: whole units of a total in a weight of one
 };
 
 __device__ __forceinline__ float2 f2(float x) { return make_float2(x, x); }
@@ -104,10 +107,23 @@ __device__ __forceinline__ float one_if(bool p, float x) {
 // The first 48 bytes of the 32 records go to shared memory by 16-byte
 // asynchronous copies, three lanes to a record; the warp evaluates all of
 // them, four per transposing butterfly, which leaves each entry's result in
-// the lane that owns the entry; that lane adds it to the Gaussian's 64-bit
-// total in units of 2^-32 -- integers, so totals do not depend on the order in
-// which warps arrive. (A maximum of non-negative floats is a maximum of their
-// bits.) The next chunk's records, the one after's ids and the next masks are
+// the lane that owns the entry; that lane adds it to the Gaussian's total --
+// integers, so totals do not depend on the order in which warps arrive. (A
+// maximum of non-negative floats is a maximum of their bits.)
+//
+// A total has 96 bits: a word of 64 in units of 2^-k and, apart, a word of 32
+// in units of 2^-(k + 32) whose carries go to the first. A pixel's weights sum
+// to one at most, so the first word holds every total of a frame with
+// pixels 2^k < 2^64 (k = 43 at 1080p, 41 at 4K). The least sum that a frame
+// without pixel weights has, 1e-4 / 255 (2^-21.3), is 2^20 whole units or more
+// up to 4K: from there on a sum is rounded to whole units, 2^-21 of it at most
+// and less than the roundings of the T it was made with, and costs one atomic.
+// Smaller sums (of small pixel weights, or of calls of more pixels) are held
+// exactly, down to 2^-(k + 9): they are the scores that an eviction orders.
+// Sending all sums below 2^23 units that way took 0.7 % more at 4K; clearing and
+// reading the second word takes 0.3 % there.
+//
+// The next chunk's records, the one after's ids and the next masks are
 // in flight meanwhile; no warp waits for another, and only the last chunk of
 // a block is padded.
 //
@@ -124,7 +140,8 @@ __device__ __forceinline__ float one_if(bool p, float x) {
 // records, 0.277 ms (a bulk copy is issued lane by lane); plain loads through
 // registers, 0.243 ms; four pixels per lane, 0.251 ms; one warp per thread
 // block, 0.233 ms.
-constexpr float kWeightUnit = 4294967296.f;  // 2^32
+constexpr float kWeightRest = 4294967296.f;  // 2^32: units of a rest in a whole one
+constexpr float kWeightWhole = 1048576.f;    // 2^20: whole units from which on rests are rounded
 constexpr int kWeightQueue = 256;            // positions a warp can hold
 constexpr int kWeightAhead = 96;             // positions it wants queued: three chunks
 constexpr int kWeightRow = 12;               // floats of a record the walk stages
@@ -135,8 +152,8 @@ __global__ void __launch_bounds__(32 * kWarps) k_blend_weights(
     const float* __restrict__ records, const uint32_t* __restrict__ ids,
     const int64_t* __restrict__ ranges, WeightGeom geo, const uint32_t* __restrict__ n_contrib,
     const uint8_t* __restrict__ wmask_in, const float* __restrict__ pixel_weight,
-    unsigned long long* __restrict__ sums, uint32_t* __restrict__ largest,
-    uint32_t* __restrict__ status) {
+    unsigned long long* __restrict__ sums, uint32_t* __restrict__ rests,
+    uint32_t* __restrict__ largest, uint32_t* __restrict__ status) {
   __shared__ __align__(16) float s_rec[kWarps][2][32][kWeightRow];
   __shared__ __align__(16) uint32_t s_at[kWarps][32];
   __shared__ uint32_t s_queue[kWarps][kWeightQueue];
@@ -311,9 +328,17 @@ __global__ void __launch_bounds__(32 * kWarps) k_blend_weights(
         if ((lane & 7) == g) top = m;
       }
     }
-    if (sum > 0.f) {  // an entry without a Gaussian sums to 0
-      atomicAdd(&sums[mine.id], __float2ull_rn(sum * kWeightUnit));
-      if (MAX) atomicMax(&largest[mine.id], __float_as_uint(top));
+    // an entry without a Gaussian sums to 0
+    const float units = sum * geo.whole;
+    if (units >= kWeightWhole) atomicAdd(&sums[mine.id], __float2ull_rn(units));
+    if (MAX && sum > 0.f) atomicMax(&largest[mine.id], __float_as_uint(top));
+    // seldom: tested for the warp (a branch per lane: 1.3 % more at 4K)
+    const bool small = units > 0.f && units < kWeightWhole;
+    if (__any_sync(0xffffffffu, small) && small) {
+      uint32_t add = __float2uint_rz(units);
+      const uint32_t rest = __float2uint_rn((units - truncf(units)) * kWeightRest);
+      if (rest && atomicAdd(&rests[mine.id], rest) + rest < rest) ++add;  // a carry
+      if (add) atomicAdd(&sums[mine.id], (unsigned long long)add);
     }
     __syncwarp();  // the chunk's shared memory is free
   }
@@ -322,23 +347,26 @@ __global__ void __launch_bounds__(32 * kWarps) k_blend_weights(
 // Before the walk: totals cleared, the kept maxima scaled (a decay of 0 reads
 // nothing). A kept maximum below zero or NaN counts as zero.
 __global__ void __launch_bounds__(256) k_weights_begin(unsigned long long* __restrict__ sums,
+                                                       uint32_t* __restrict__ rests,
                                                        float* __restrict__ largest, int n,
                                                        float decay) {
   let_next_begin();
   const int i = blockIdx.x * 256 + threadIdx.x;
   if (i >= n) return;
   sums[i] = 0ull;
+  rests[i] = 0u;
   if (largest) largest[i] = decay > 0.f ? fmaxf(decay * largest[i], 0.f) : 0.f;
 }
 
 // After the walk: sum <- decay sum + total, in double, rounded once.
 __global__ void __launch_bounds__(256) k_weights_end(const unsigned long long* __restrict__ sums,
+                                                     const uint32_t* __restrict__ rests,
                                                      float* __restrict__ weight_sum, int n,
-                                                     float decay) {
+                                                     double unit, float decay) {
   wait_for_previous();
   const int i = blockIdx.x * 256 + threadIdx.x;
   if (i >= n) return;
-  const double t = (double)sums[i] * (1.0 / 4294967296.0);
+  const double t = fma((double)rests[i], 1.0 / (double)kWeightRest, (double)sums[i]) * unit;
   weight_sum[i] = (float)(decay > 0.f ? fma((double)decay, (double)weight_sum[i], t) : t);
 }
 
@@ -353,8 +381,14 @@ cudaError_t launch_blend_weights(const float* records, const uint32_t* ids, cons
   const int64_t tiles = (int64_t)g.tiles_per_view * n_views;
   const unsigned blocks = (unsigned)(((int64_t)n + 255) / 256);
   unsigned long long* acc = reinterpret_cast<unsigned long long*>(sums);
-  k_weights_begin<<<blocks, 256, 0, stream>>>(acc, weight_max, n, decay);
-  WeightGeom geo{g, n, capacity};
+  uint32_t* rests = reinterpret_cast<uint32_t*>(acc + n);
+  // the largest 2^k by which the pixels, 2^31 at most, fit 64 bits; 2^-10 of
+  // them are left to the roundings of the weights and their sums
+  const uint64_t pixels = (uint64_t)g.width * g.height * n_views;
+  int k = 63;
+  while (pixels > (0ull - (1ull << 54)) >> k) --k;
+  k_weights_begin<<<blocks, 256, 0, stream>>>(acc, rests, weight_max, n, decay);
+  WeightGeom geo{g, n, capacity, ldexpf(1.f, k)};
   const auto walk = warp_masks ? (weight_max ? k_blend_weights<true, true>
                                              : k_blend_weights<true, false>)
                                : (weight_max ? k_blend_weights<false, true>
@@ -362,11 +396,12 @@ cudaError_t launch_blend_weights(const float* records, const uint32_t* ids, cons
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess)
     e = launch_dependent(walk, dim3((unsigned)tiles), dim3(32 * kWarps), stream, records,
-                         ids, ranges, geo, n_contrib, warp_masks, pixel_weight, acc,
+                         ids, ranges, geo, n_contrib, warp_masks, pixel_weight, acc, rests,
                          reinterpret_cast<uint32_t*>(weight_max), status);
   if (e == cudaSuccess)
     e = launch_dependent(k_weights_end, dim3(blocks), dim3(256), stream,
-                         (const unsigned long long*)acc, weight_sum, n, decay);
+                         (const unsigned long long*)acc, (const uint32_t*)rests, weight_sum, n,
+                         ldexp(1.0, -k), decay);
   return e;
 }
 

@@ -517,9 +517,12 @@ size_t gs_blend_weights_workspace_size(int64_t n);
  *   weight_sum    float [n]
  *   weight_max    float [n], NULL skips it; a kept maximum below 0 or NaN
  *                 counts as 0
- * The sums of a call are held in 64-bit fixed point (units of 2^-32) and the
- * step above is taken in double and rounded once, so results do not depend on
- * the order in which tiles run: the same inputs give the same bits. The status
+ * The float sums of the 8 x 8 pixel blocks are added up as integers of 96
+ * bits, so results do not depend on the order in which tiles run: the same
+ * inputs give the same bits. With k the largest for which n_views H W 2^k is
+ * at most 2^64 - 2^54 (63 at most; 43 at 1920 x 1080), a block's sum of
+ * 2^(20 - k) or more is rounded to 2^-k, a smaller one to 2^-(k + 32).
+ * The step above is then taken in double and rounded once. The status
  * word of `ws` (gs_blend_weights_workspace_size(n) bytes) receives
  * GS_STATUS_BIT_BOUNDS for an entry it has to read that names a Gaussian >= n
  * (the entry adds nothing) or a tile range outside the ids buffer (the tile
