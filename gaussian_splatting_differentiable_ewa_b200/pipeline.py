@@ -676,7 +676,8 @@ class Splatter:
         """Add the blending weights of the last rendered frame (forward,
         rasterize_fwd, a training step) to ``self.weight_sum``, scaled by
         `decay` first, and with `largest` their maxima to ``self.weight_max``
-        (gs_blend_weights). pixel_weight: float32 [V, H, W] in [0, 1], a mask
+        (gs_blend_weights). Maxima that an earlier call began are scaled and
+        kept up by every call, so that both scores forget alike. pixel_weight: float32 [V, H, W] in [0, 1], a mask
         or an error map. Both start from zero and restart with every new
         Gaussian set. Once project, bin_sort or ensure_capacity has run after
         the render, or the buffers were reallocated, the frame is gone and a
@@ -698,7 +699,7 @@ class Splatter:
                 self.weight_max = torch.zeros(self.n, dtype=torch.float32, device=self.device)
         api.gs_blend_weights(self.c_proj, self.c_bins, self.cams, self.V, self.n, self.n_contrib,
                              self.weight_sum, self._weights_ws,
-                             weight_max=self.weight_max if largest else None,
+                             weight_max=self.weight_max,
                              warp_masks=self.warp_masks, pixel_weight=pixel_weight, decay=decay,
                              stream=self.stream)
         return self.weight_sum

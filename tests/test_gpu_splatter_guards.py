@@ -80,3 +80,21 @@ def test_host_fed_paths_leave_a_frame():
                     sp.accumulate_weights(decay=0.0)
     torch.cuda.synchronize()
     assert sp.status() == api.GS_OK and sp.weights_status() == api.GS_OK
+
+
+def test_sums_and_maxima_tell_of_the_same_frames():
+    """A call without `largest` after one with it forgets and adds the same in
+    both scores."""
+    sp = _splatter()
+    pw = torch.zeros((1, sp.H, sp.W), device="cuda")
+    pw[:, :, : sp.W // 2] = 1.0
+    sp.accumulate_weights(pixel_weight=pw, largest=True)
+    sums, tops = sp.weight_sum.clone(), sp.weight_max.clone()
+    sp.accumulate_weights(pixel_weight=1.0 - pw, decay=0.25)
+    ws = torch.zeros_like(sp._weights_ws)
+    api.gs_blend_weights(sp.c_proj, sp.c_bins, sp.cams, sp.V, sp.n, sp.n_contrib, sums, ws,
+                         weight_max=tops, warp_masks=sp.warp_masks, pixel_weight=1.0 - pw,
+                         decay=0.25)
+    assert torch.equal(sp.weight_sum, sums) and torch.equal(sp.weight_max, tops)
+    # a sum holds its largest term but for its last roundings (2^-21 + 2^-23)
+    assert torch.all(sp.weight_max <= sp.weight_sum * (1.0 + 2.0 ** -20))

@@ -43,3 +43,18 @@ def test_new_lists_beside_an_old_frame_are_refused(logged):
     sp.rasterize_fwd()
     sp.accumulate_weights()
     assert log[-1][0] == "gs_blend_weights"
+
+
+def test_maxima_once_kept_are_kept_up(logged):
+    """From the first call with largest=True on, every call decays and raises
+    the maxima as it does the sums."""
+    sp, log = logged
+    sp.rasterize_fwd()
+    sp.accumulate_weights(decay=0.5)
+    assert sp.weight_max is None and log[-1][1]["weight_max"] is None
+    sp.accumulate_weights(decay=0.5, largest=True)
+    kept = sp.weight_max
+    assert kept is not None and log[-1][1]["weight_max"] is kept
+    sp.accumulate_weights(decay=0.5)
+    assert sp.weight_max is kept and log[-1][1]["weight_max"] is kept
+    assert log[-1][1]["decay"] == 0.5
