@@ -71,6 +71,18 @@ def allreduce_grads(flat, group=None) -> None:
         dist.all_reduce(flat, op=dist.ReduceOp.SUM, group=group)
 
 
+def same_on_all_ranks(values, device=None, group=None) -> bool:
+    """Whether every rank passed the same whole numbers (one collective; True
+    without other ranks)."""
+    import torch
+    import torch.distributed as dist
+    if not (dist.is_available() and dist.is_initialized()) or dist.get_world_size(group) < 2:
+        return True
+    t = torch.tensor([[int(v), -int(v)] for v in values], dtype=torch.int64, device=device)
+    dist.all_reduce(t, op=dist.ReduceOp.MAX, group=group)
+    return all(hi == -lo for hi, lo in t.tolist())
+
+
 def gather_for_densify(stats, flats, bounds=None, group=None) -> None:
     """Before densify_and_prune on several ranks: sum each statistics tensor
     in `stats` over the ranks (every rank then decides alike) and, when the

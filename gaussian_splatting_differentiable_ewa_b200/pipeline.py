@@ -355,13 +355,32 @@ class Splatter:
                 None if sh is None else (sh["lo"], sh["hi"]),
                 None if sh is None else sh["group"])
 
-    def _gather_for_evict(self, with_weights: bool) -> None:
-        """Before evict on several ranks: the summed blending weights and, when
-        the optimiser is sharded, every rank's slice of the moments."""
+    def _gather_for_evict(self, with_weights: bool) -> Optional[torch.Tensor]:
+        """Before evict on several ranks: every rank's slice of the moments when
+        the optimiser is sharded, and the blending weights summed in a tensor of
+        their own, which is returned (this rank's stay what it accumulated)."""
         sh = self._shard
+        score = self.weight_sum.clone() if with_weights else None
         gdist.gather_for_densify(
-            (self.weight_sum,) if with_weights else (), (self.m_flat, self.v_flat),
+            (score,) if with_weights else (), (self.m_flat, self.v_flat),
             None if sh is None else (sh["lo"], sh["hi"]), None if sh is None else sh["group"])
+        return score
+
+    def _check_evict(self, n_keep: int, score, protect) -> Optional[str]:
+        """Why evict cannot take these arguments, or None."""
+        n = self.n
+        if n_keep < 1:
+            return "n_keep must be at least 1"
+        if score is None and self.weight_sum is None:
+            return "no score: call accumulate_weights first or give one"
+        if score is not None and (tuple(score.shape) != (n,) or score.dtype != torch.float32
+                                  or score.device != self.ws.device):
+            return "score must be float32 [n] on the device"
+        if protect is not None and (tuple(protect.shape) != (n,)
+                                    or protect.dtype not in (torch.uint8, torch.bool)
+                                    or protect.device != self.ws.device):
+            return "protect must be uint8 or bool [n] on the device"
+        return None
 
     def _graph_of(self, fn, note=None) -> "torch.cuda.CUDAGraph":
         """A CUDA graph of one fixed-shape call: run once outside capture (on
@@ -719,27 +738,29 @@ class Splatter:
         gs_densify_sh_quant), every per-Gaussian buffer is reallocated and the
         statistics and weights restart from zero. On several ranks the
         accumulated weights are summed first, so that every rank evicts
-        alike; a `score` or `protect` given must be the same on all of them.
+        alike; a `score` or `protect` given must be the same on all of them,
+        and arguments that one rank cannot take raise on every rank (with a
+        `score` and an optimiser that is not sharded nothing is exchanged).
+        Weights and set stay as they were where an error is raised.
         Returns the decisions (int8 [n], 1 kept)."""
         n, dev = self.n, self.device
         n_keep = int(n_keep)
-        if n_keep < 1:
-            raise ValueError("n_keep must be at least 1")
-        if score is None and self.weight_sum is None:
-            raise ValueError("no score: call accumulate_weights first or give one")
-        if score is not None and (tuple(score.shape) != (n,) or score.dtype != torch.float32
-                                  or score.device != self.ws.device):
-            raise ValueError("score must be float32 [n] on the device")
-        if protect is not None and (tuple(protect.shape) != (n,)
-                                    or protect.dtype not in (torch.uint8, torch.bool)
-                                    or protect.device != self.ws.device):
-            raise ValueError("protect must be uint8 or bool [n] on the device")
+        refusal = self._check_evict(n_keep, score, protect)
+        alike = True
+        if score is None or self._shard is not None:
+            # collectives follow: what the ranks do has to be the same, an error too
+            with self._torch_stream():
+                alike = gdist.same_on_all_ranks(
+                    (refusal is None, n, min(n, max(n_keep, 0)), score is None, protect is None),
+                    self.ws.device, None if self._shard is None else self._shard["group"])
+        if refusal is not None or not alike:
+            raise ValueError(refusal or "the ranks' sets or their arguments of evict differ")
         quant = self.sh_bits is not None
         names = [k for k, _ in self.param_list]
         m = min(n, n_keep)
         with self._torch_stream():
-            self._gather_for_evict(with_weights=score is None)
-            score = (self.weight_sum if score is None else score).contiguous()
+            summed = self._gather_for_evict(with_weights=score is None)
+            score = (summed if score is None else score).contiguous()
             protect = None if protect is None else protect.contiguous()
 
             def like(t):

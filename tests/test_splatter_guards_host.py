@@ -1,12 +1,21 @@
 """What Splatter.accumulate_weights and Splatter.evict keep track of on the
-host, with the C calls replaced by a log: which frame the buffers hold."""
+host, with the C calls replaced: which frame the buffers hold, which scores are
+kept up, and what several ranks agree on before they evict."""
 
+import datetime
+import os
+import socket
+
+import numpy as np
 import pytest
 import torch
+import torch.distributed as dist
+import torch.multiprocessing as mp
 
 from gaussian_splatting_differentiable_ewa_b200 import api
 from gaussian_splatting_differentiable_ewa_b200 import scenes as S
 from gaussian_splatting_differentiable_ewa_b200.pipeline import Splatter
+from oracle import oracle as O
 
 CALLS = ("gs_project", "gs_bin_sort", "gs_rasterize_fwd", "gs_rasterize_bwd", "gs_densify_stats",
          "gs_project_bwd_adam", "gs_adam_step", "gs_l1_dssim", "gs_blend_weights")
@@ -58,3 +67,81 @@ def test_maxima_once_kept_are_kept_up(logged):
     sp.accumulate_weights(decay=0.5)
     assert sp.weight_max is kept and log[-1][1]["weight_max"] is kept
     assert log[-1][1]["decay"] == 0.5
+
+
+def _free_port() -> int:
+    with socket.socket() as s:
+        s.bind(("127.0.0.1", 0))
+        return s.getsockname()[1]
+
+
+def _rank_worker(rank, world, port, out):
+    """Evictions that one rank cannot take, then one whose status is an error,
+    then the same again: the kernels replaced by the oracle's order."""
+    os.environ["MASTER_ADDR"], os.environ["MASTER_PORT"] = "127.0.0.1", str(port)
+    dist.init_process_group("gloo", rank=rank, world_size=world,
+                            timeout=datetime.timedelta(seconds=20))
+    n, status, seen = 40, [api.GS_OK], {}
+
+    def select(score, protect, n_, n_keep, decisions, ws, stream=None):
+        seen["score"] = score.tolist()
+        decisions.copy_(torch.from_numpy(O.evict_select(score.numpy(), None, n_keep)))
+
+    api.gs_evict_select = select
+    api.gs_evict_compact = lambda *a, **k: None
+    api.gs_get_status = lambda ws, stream=None: status[0]
+    sp = Splatter(S.make_scene("fwd_1k_128", n=n), device="cpu")
+    sp.shard_optimizer(rank, world)
+    mine = torch.arange(n, dtype=torch.float32) * (1.0 if rank == 0 else -2.0)
+    first = rank == 0
+
+    def refused(*a, **k):
+        try:
+            sp.evict(*a, **k)
+        except ValueError as e:
+            return str(e)
+        return None
+
+    # no rank, then only the first one has accumulated weights
+    raised = [refused(10)]
+    sp.weight_sum = mine.clone() if first else None
+    raised.append(refused(10))
+    sp.weight_sum = mine.clone()
+    # a budget, a score or a protection that only one rank has, or has wrong
+    raised += [refused(10 if first else 0), refused(10 if first else 11),
+               refused(10, score=mine if first else None),
+               refused(10, score=mine if first else mine[:3]),
+               refused(10, protect=torch.zeros(n, dtype=torch.uint8) if first else None)]
+    kept = torch.equal(sp.weight_sum, mine)
+    # selection reports an error on every rank: their own totals stay
+    status[0] = api.GS_ERR_DEVICE_TIMEOUT
+    try:
+        sp.evict(10)
+        failed = False
+    except api.GsError:
+        failed = True
+    kept = kept and torch.equal(sp.weight_sum, mine)
+    status[0] = api.GS_OK
+    # a score and an optimiser of its own: no rank waits for another
+    alone = Splatter(S.make_scene("fwd_1k_128", n=n + rank), device="cpu")
+    if first:
+        alone.evict(10, score=torch.arange(n + rank, dtype=torch.float32))
+    d = sp.evict(10)
+    out.put((rank, dict(raised=raised, kept=kept, failed=failed, d=d.tolist(), n=sp.n,
+                        score=seen["score"])))
+    dist.barrier()
+    dist.destroy_process_group()
+
+
+def test_ranks_refuse_and_retry_alike():
+    ctx = mp.get_context("spawn")
+    out = ctx.SimpleQueue()
+    mp.spawn(_rank_worker, args=(2, _free_port(), out), nprocs=2, join=True)
+    got = dict(out.get() for _ in range(2))
+    for rank in range(2):
+        r = got[rank]
+        assert all(r["raised"]), r["raised"]
+        assert "accumulate_weights" in r["raised"][0]
+        assert r["kept"] and r["failed"] and r["n"] == 10
+        assert r["score"] == [-float(i) for i in range(40)]
+        assert r["d"] == np.repeat([1, 0], [10, 30]).tolist()
