@@ -325,6 +325,20 @@ class Splatter:
         return (torch.cuda.stream(self.stream) if self.stream is not None
                 else contextlib.nullcontext())
 
+    def _from_caller(self, *tensors) -> None:
+        """Tensors that the caller made on its current stream: ``self.stream``
+        waits for what is on that stream now, and their memory is not handed out
+        again before the calls that read them are done. (While the current
+        stream is captured, the caller orders the two.)"""
+        cur = torch.cuda.current_stream(self.device) if self.stream is not None else None
+        given = [t for t in tensors if t is not None]
+        if (cur is None or cur == self.stream or not given
+                or torch.cuda.is_current_stream_capturing()):
+            return
+        self.stream.wait_stream(cur)
+        for t in given:
+            t.record_stream(self.stream)
+
     def _sharded_adam_step(self, beta1, beta2, eps) -> None:
         import torch.distributed as dist
         sh = self._shard
@@ -701,7 +715,9 @@ class Splatter:
         Gaussian set. Once project, bin_sort or ensure_capacity has run after
         the render, or the buffers were reallocated, the frame is gone and a
         ValueError asks for the next one; replays of capture_calls' graphs
-        count as their calls, graphs that the caller captured are not seen."""
+        count as their calls, graphs that the caller captured are not seen.
+        With a stream of its own the Splatter waits for pixel_weight on the
+        caller's current stream; the result is complete on ``self.stream``."""
         if getattr(self, "_frame_gen", None) != self._gen:
             raise ValueError("the buffers hold no whole frame: render one first")
         if pixel_weight is not None and (tuple(pixel_weight.shape) != (self.V, self.H, self.W)
@@ -709,6 +725,7 @@ class Splatter:
                                          or pixel_weight.device != self.ws.device
                                          or not pixel_weight.is_contiguous()):
             raise ValueError("pixel_weight must be contiguous float32 [V, H, W] on the device")
+        self._from_caller(pixel_weight)
         with self._torch_stream():
             if self.weight_sum is None:
                 self.weight_sum = torch.zeros(self.n, dtype=torch.float32, device=self.device)
@@ -741,7 +758,9 @@ class Splatter:
         alike; a `score` or `protect` given must be the same on all of them,
         and arguments that one rank cannot take raise on every rank (with a
         `score` and an optimiser that is not sharded nothing is exchanged).
-        Weights and set stay as they were where an error is raised.
+        Weights and set stay as they were where an error is raised. With a
+        stream of its own the Splatter waits for `score` and `protect` on the
+        caller's current stream.
         Returns the decisions (int8 [n], 1 kept)."""
         n, dev = self.n, self.device
         n_keep = int(n_keep)
@@ -758,6 +777,7 @@ class Splatter:
         quant = self.sh_bits is not None
         names = [k for k, _ in self.param_list]
         m = min(n, n_keep)
+        self._from_caller(score, protect)
         with self._torch_stream():
             summed = self._gather_for_evict(with_weights=score is None)
             score = (summed if score is None else score).contiguous()

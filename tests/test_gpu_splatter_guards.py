@@ -98,3 +98,40 @@ def test_sums_and_maxima_tell_of_the_same_frames():
     assert torch.equal(sp.weight_sum, sums) and torch.equal(sp.weight_max, tops)
     # a sum holds its largest term but for its last roundings (2^-21 + 2^-23)
     assert torch.all(sp.weight_max <= sp.weight_sum * (1.0 + 2.0 ** -20))
+
+
+def test_inputs_from_another_stream_are_waited_for():
+    """A Splatter on a stream of its own, pixel weights, scores and protection
+    still being computed on the caller's stream, and let go of after the call."""
+    stream = torch.cuda.Stream()
+    sp = _splatter(stream=stream)
+    with torch.cuda.stream(stream):
+        want = sp.accumulate_weights(decay=0.0).clone()
+    torch.cuda.synchronize()
+
+    def late(shape, dtype, value):
+        t = torch.zeros(shape, dtype=dtype, device="cuda")
+        torch.cuda._sleep(40_000_000)          # some 20 ms
+        return t.copy_(value)
+
+    shape = (sp.V, sp.H, sp.W)
+    ones = torch.ones(shape, device="cuda")
+    # the memory of weights let go of is not handed out while they are read
+    for _ in range(3):
+        got = sp.accumulate_weights(pixel_weight=late(shape, torch.float32, ones), decay=0.0)
+        with torch.cuda.stream(stream):
+            first = got.clone()
+            torch.cuda._sleep(40_000_000)
+        sp.accumulate_weights(pixel_weight=ones.clone(), decay=0.0)
+        other = [torch.zeros(shape, device="cuda") for _ in range(8)]
+        torch.cuda.synchronize()
+        assert torch.equal(first, want) and torch.equal(got, want) and not any(bool(o.any()) for o in other)
+    n, keep = sp.n, 700
+    values = torch.arange(n, dtype=torch.float32, device="cuda")
+    marked = values < 3
+    d = sp.evict(keep, score=late((n,), torch.float32, values),
+                 protect=late((n,), torch.bool, marked))
+    torch.cuda.synchronize()
+    rows = torch.nonzero(d)[:, 0]
+    assert torch.equal(rows, torch.cat([torch.arange(3, device="cuda"),
+                                        torch.arange(n - keep + 3, n, device="cuda")]))
