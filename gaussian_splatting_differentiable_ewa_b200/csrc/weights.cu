@@ -95,11 +95,12 @@ __device__ __forceinline__ float one_if(bool p, float x) {
 
 // Accumulated blending weights (gs_blend_weights): per list entry the sum (and
 // with MAX the largest) over a tile's pixels of m w, w = alpha T the forward's
-// weight and m the pixel's weight in [0, 1]. The walk evaluates what the
-// forward evaluates (the same IEEE operations) without colours and without its
-// stop test: n_contrib already says how far each pixel composited. The weights
-// are linear in T, so T starts at m and the pixel weight costs nothing per
-// entry.
+// weight and m the pixel's weight in [0, 1]. The walk takes zq and alpha by the
+// forward's IEEE operations, without colours and without its stop test:
+// n_contrib already says how far each pixel composited. T falls by one fma,
+// T - alpha T, where the forward rounds 1 - alpha and then T (1 - alpha), so
+// that weights are the forward's but for a rounding of T per entry. They are
+// linear in T, so T starts at m and the pixel weight costs nothing per entry.
 //
 // Every warp works by itself on its 8 x 8 pixel block, two pixels per lane:
 // it scans the list for the entries that reach its block (the forward's masks,
@@ -114,12 +115,13 @@ __device__ __forceinline__ float one_if(bool p, float x) {
 // A total has 96 bits: a word of 64 in units of 2^-k and, apart, a word of 32
 // in units of 2^-(k + 32) whose carries go to the first. A pixel's weights sum
 // to one at most, so the first word holds every total of a frame with
-// pixels 2^k < 2^64 (k = 43 at 1080p, 41 at 4K). The least sum that a frame
-// without pixel weights has, 1e-4 / 255 (2^-21.3), is 2^20 whole units or more
-// up to 4K: from there on a sum is rounded to whole units, 2^-21 of it at most
-// and less than the roundings of the T it was made with, and costs one atomic.
-// Smaller sums (of small pixel weights, or of calls of more pixels) are held
-// exactly, down to 2^-(k + 9): they are the scores that an eviction orders.
+// pixels 2^k < 2^64 (k = 43 at 1080p, 41 at 4K). From 2^20 whole units on a sum
+// is rounded to them, 2^-21 of it at most, less than the roundings of the T
+// that a weak sum was made with, and costs one atomic; the least sum that a
+// frame without pixel weights has, 1e-4 / 255 (2^-21.3), lies above that at
+// 1080p and just below at 4K. Smaller sums (of small pixel weights, or of calls
+// of more pixels) are held exactly, down to 2^-(k + 9): they are the scores
+// that an eviction orders.
 // Sending all sums below 2^23 units that way took 0.7 % more at 4K; clearing and
 // reading the second word takes 0.3 % there.
 //
@@ -133,7 +135,7 @@ __device__ __forceinline__ float one_if(bool p, float x) {
 // pairs would take 18). On a 1M-Gaussian 1080p frame (4.4M entries of 8 x 8
 // blocks) the whole call takes 0.230 ms at 82 % of the issue slots, the
 // forward itself 0.494 ms; on 1000 Gaussians at 128 x 128 three launches take
-// 0.013 ms (0.015 before the walk and the last kernel were allowed to begin
+// 0.015 ms (0.002 more before the walk and the last kernel were allowed to begin
 // while the kernel before them ends). What was measured on the way, for the
 // 1080p frame: a block staging batches of its tile's list as the forward
 // does, 0.290 ms (barriers, and lists padded per batch); bulk copies of the
